@@ -356,6 +356,177 @@ int stagq_check(stagq_handle h);
 
 int stagq_info(stagq_handle h, stagq_info_t* info);
 
+/* ============================================================= operators
+ *
+ * Operators that stand beside the GEMV in a served model: the linear layer
+ * for more tokens than the GEMV takes, and the 4-bit cache that its q, k and v
+ * feed. All of them
+ *   - are asynchronous on `cuda_stream` of GPU `device` (any device may be
+ *     current), allocate nothing and can be captured in a CUDA graph;
+ *   - take 16-bit tensors as fp16, or as bf16 with STAGQ_BF16;
+ *   - take rows that lie `stride` elements apart (a slice of a stacked q/k/v
+ *     result, for instance); rows on 16 bytes are read with wide loads;
+ *   - report what only the GPU can see (a page number outside the pool, a
+ *     wait that ran out) through stagq_ops_check, and never read or write
+ *     outside the caller's buffers because of it.
+ * Outputs must not overlap inputs.
+ */
+#define STAGQ_BF16 16u           /* the 16-bit tensors of the call are bf16 */
+
+#define STAGQ_I8_ROW_MULTIPLE 128 /* rows of 8-bit values are padded with zeros to this many bytes */
+#define STAGQ_KV_MAX_NEW 16      /* newest tokens of a sequence in one attention call */
+#define STAGQ_KV_MAX_SHARE 64    /* query heads per KV head */
+#define STAGQ_KV_MAX_TOKENS (1 << 30) /* positions of one sequence */
+
+/* Bytes of one row of `in` 8-bit values: in rounded up to
+ * STAGQ_I8_ROW_MULTIPLE; -1 unless 1 <= in <= STAGQ_MAX_IN. */
+int64_t stagq_i8_row_bytes(int32_t in);
+
+/*
+ * Rows rounded to 8 bits with a scale each (activations: a scale per token;
+ * weights [out, in]: a scale per output channel):
+ *   a_i = max_k |x_ik|,  scale_i = a_i / 127,  q_ik = rint(127 x_ik / a_i)
+ * with ties to even on the binary64 quotient; a_i = 0 gives q = 0. A row that
+ * holds an infinity or a NaN gets scale NaN and q = 0, so that every product
+ * with it is NaN.
+ *   x      device [n] rows of `in` 16-bit values, x_stride elements apart
+ *   q      device [n] rows of stagq_i8_row_bytes(in) bytes (16-byte aligned);
+ *          bytes from `in` on are set to 0
+ *   scale  device [n] fp32
+ * flags: STAGQ_BF16. Errors: STAGQ_EINVAL, STAGQ_ECUDA.
+ */
+int stagq_quantize_i8(const void* x, int64_t x_stride, int32_t n, int32_t in, uint32_t flags, int8_t* q,
+                      float* scale, int device, void* cuda_stream);
+
+/*
+ * y_ij = xscale_i wscale_j sum_k xq_ik wq_jk for i < n, j < out: the sum is
+ * exact (int32), scaled in fp32 and rounded once.
+ *   xq, wq  device rows of stagq_i8_row_bytes(in) bytes, 16-byte aligned, whose
+ *           bytes from `in` on are 0 (as stagq_quantize_i8 leaves them)
+ *   y       device [n] rows of `out` values, y_stride elements apart: fp16,
+ *           bf16 (STAGQ_BF16) or fp32 (STAGQ_Y_F32)
+ * Uses no workspace: calls may run concurrently. The result does not depend on
+ * how the work is split. Errors: STAGQ_EINVAL, STAGQ_ECUDA.
+ */
+int stagq_gemm_i8(const int8_t* xq, const float* xscale, int32_t n, const int8_t* wq, const float* wscale,
+                  int32_t out, int32_t in, void* y, int64_t y_stride, uint32_t flags, int device,
+                  void* cuda_stream);
+
+/*
+ * A cache of K and V in 4 bits, held in pages of `page` tokens. The caller
+ * owns the pool and the page tables; `pages` holds n_pages pages of
+ * stagq_kv_page_bytes() bytes. Inside a page, for each KV head and for K then
+ * V, there is one block: `page` rows of dim / 2 code bytes, then `page` rows
+ * of dim / group pairs (scale, lowest) of 16-bit values. A group of `group`
+ * consecutive channels x of one token is stored as
+ *   lo = min x,  s = RN16((max x - min x) / 15),  u = clamp(rint((x - lo) / s), 0, 15)
+ * (binary64 quotients, ties to even; s = 0: u = 0) and stands for lo + s u. A
+ * group with an infinity or a NaN is stored as s = lo = NaN.
+ * A K row holds channel 32 j + 8 t + i in nibble i (low first) of the 4 bytes
+ * at t dim / 8 + 4 j; a V row holds channel 32 j + 4 g + i in nibble i of the
+ * 2 bytes at g dim / 16 + 2 j.
+ */
+typedef struct {
+    void* pages;                 /* device, 16-byte aligned */
+    int32_t n_pages, heads, dim, page, group;  /* dim 64 or 128; page a power of two, 16..1024; group 32, 64 or 128, at most dim */
+    uint32_t flags;              /* STAGQ_BF16: K, V, q, out and the stored pairs are bf16, else fp16 */
+    int32_t device;
+} stagq_kv_cache;
+
+/*
+ * Page table of one call: row b (row_stride entries apart) lists the pages of
+ * sequence b in order; position p of it is in page p / page. `width` entries
+ * of a row are the caller's; only those that hold a position in use are read.
+ */
+typedef struct {
+    const int32_t* pages;        /* device */
+    int64_t row_stride;
+    int32_t batch, width;
+} stagq_kv_table;
+
+/* Bytes of one page; -1 if the cache's dim, group or page is out of range. */
+int64_t stagq_kv_page_bytes(const stagq_kv_cache* cache);
+
+/*
+ * Rounds n new tokens of every sequence to 4 bits and writes them at positions
+ * starts[b] .. starts[b] + n - 1. Row b * n + i of k and v ([heads * dim]
+ * values, k_stride / v_stride elements apart) is token i of sequence b. A
+ * sequence with starts[b] < 0 is left alone (padding of a batch). A position
+ * past the table's width, or whose page number is not in the pool, is not
+ * written and is reported by stagq_ops_check (STAGQ_EFORMAT).
+ * Errors: STAGQ_EINVAL, STAGQ_ECUDA.
+ */
+int stagq_kv_append(const stagq_kv_cache* cache, const stagq_kv_table* table, const int32_t* starts, const void* k,
+                    int64_t k_stride, const void* v, int64_t v_stride, int32_t n, void* cuda_stream);
+
+/*
+ * The values lo + s u of positions starts[b] + i, i < n (starts null: from 0),
+ * as rows b * n + i of k and v: 16-bit, or fp32 with STAGQ_Y_F32. Rows at
+ * positions below 0, at or past lens[b] (lens null: no bound), or on a page
+ * that is not in the pool, are zero. Errors: as stagq_kv_append.
+ */
+int stagq_kv_read(const stagq_kv_cache* cache, const stagq_kv_table* table, const int32_t* starts,
+                  const int32_t* lens, void* k, int64_t k_stride, void* v, int64_t v_stride, int32_t n, uint32_t flags,
+                  void* cuda_stream);
+
+/*
+ * Attention of the n_new newest tokens of every sequence over its cache, which
+ * holds them already: lens[b] is its number of cached tokens. Query head i
+ * reads KV head i / (q_heads / heads). Token j (0 .. n_new - 1) sees the first
+ * lens[b] - (n_new - 1 - j) positions; one that sees none gets zeros.
+ *   out = sum_t softmax(scale q . K_t)_t V_t
+ *   q, out    device rows b * n_new + j of [q_heads * dim] values
+ *   max_len   at least every lens[b], at most width * page and
+ *             STAGQ_KV_MAX_TOKENS; the split of the work is laid out for it
+ *             (a captured graph stays right as the sequences grow up to it). A longer
+ *             sequence is cut to max_len and reported (STAGQ_EFORMAT).
+ *   mass      null, or fp32 [batch, heads, >= max_len] with the two strides: the
+ *             weights that position t got from the call's query rows of that KV
+ *             head are added to mass[b, h, t], in a fixed order. Positions past
+ *             lens[b] are left as they were.
+ *   workspace device, 256-byte aligned, of at least
+ *             stagq_kv_attention_workspace() bytes (may be null if that is 0).
+ *             Calls that run at the same time need workspaces of their own.
+ * A position whose page is not in the pool counts as unseen and is reported.
+ * Errors: STAGQ_EINVAL, STAGQ_ECUDA.
+ */
+int stagq_kv_attention(const stagq_kv_cache* cache, const stagq_kv_table* table, const int32_t* lens, int32_t max_len,
+                       const void* q, int64_t q_stride, int32_t q_heads, int32_t n_new, float scale, void* out,
+                       int64_t out_stride, float* mass, int64_t mass_stride_b, int64_t mass_stride_h, void* workspace,
+                       int64_t workspace_bytes, void* cuda_stream);
+
+/* Workspace bytes of such a call (`tracked`: with a mass); -1 for bad arguments. */
+int64_t stagq_kv_attention_workspace(const stagq_kv_cache* cache, int32_t batch, int32_t max_len, int32_t q_heads,
+                                     int32_t n_new, int tracked);
+
+/*
+ * Thins every sequence out to `budget` tokens: per KV head the last `recent`
+ * ones and, of those before them, the budget - recent of the largest mass (ties
+ * to the lowest position, a NaN counts as the largest), copied in their order
+ * to positions 0, 1, ... of the pages in `fresh`. Those must be none of the
+ * pages that `table` lists; the old pages are only read, so other sequences may
+ * share them. Sequences of at most `budget` tokens are copied whole.
+ *   mass      fp32 [batch, heads, >= max_len]
+ *   kept      device int32 [batch, heads, budget]: the old position of each
+ *             kept token, -1 past the last
+ *   new_lens  device int32 [batch]: min(lens[b], budget)
+ *   new_mass  fp32 [batch, heads, new_cap] (budget <= new_cap): the kept
+ *             tokens' masses, then zeros
+ * lens, max_len: as stagq_kv_attention. Errors: STAGQ_EINVAL, STAGQ_ECUDA.
+ */
+int stagq_kv_evict(const stagq_kv_cache* cache, const stagq_kv_table* table, const int32_t* lens, int32_t max_len,
+                   const float* mass, int64_t mass_stride_b, int64_t mass_stride_h, int32_t budget, int32_t recent,
+                   const stagq_kv_table* fresh, int32_t* kept, int32_t* new_lens, float* new_mass,
+                   int64_t new_mass_stride_b, int64_t new_mass_stride_h, int32_t new_cap, void* cuda_stream);
+
+/*
+ * Waits for the device and reports what the operators' kernels on it noted
+ * since the last call: STAGQ_EFORMAT (a page number, position or length
+ * outside the pool, the table or max_len), STAGQ_ETIMEOUT (a bounded wait ran
+ * out; the output is undefined), or STAGQ_ECUDA. Clears what it reports.
+ */
+int stagq_ops_check(int device);
+
 /* ------------------------------------------------------------ test hooks */
 
 /*

@@ -1,8 +1,9 @@
-"""StagQ multi-precision batch-one GEMV on B200 (sm_100a).
+"""StagQ multi-precision batch-one GEMV on B200 (sm_100a), and the serving
+operators beside it: the 8-bit linear and the 4-bit cache.
 
 Thin ctypes binding of ``libstagq.so`` (see ``include/stagq.h``): the
 functions below carry the C ABI's names and only marshal arguments. Every
-step of the GEMV runs in the library's CUDA kernels; PyTorch is used only for
+step of an operator runs in the library's CUDA kernels; PyTorch is used only for
 device memory and streams. If the library is missing this package raises --
 there is no fallback implementation.
 """
@@ -29,6 +30,11 @@ STAGQ_MAX_PLANES = 4
 STAGQ_MAX_BATCH = 4
 STAGQ_MAX_STACK = 4
 STAGQ_MAX_MANY = 1024
+STAGQ_BF16 = 16
+STAGQ_I8_ROW_MULTIPLE = 128
+STAGQ_KV_MAX_NEW = 16
+STAGQ_KV_MAX_SHARE = 64
+STAGQ_KV_MAX_TOKENS = 1 << 30
 
 _c_p = ctypes.c_void_p
 _i32, _i64, _u32, _dbl = ctypes.c_int32, ctypes.c_int64, ctypes.c_uint32, ctypes.c_double
@@ -57,6 +63,17 @@ class _Info(ctypes.Structure):
                 ("device", _i32), ("device_bytes", _i64)]
 
 
+class _KvCache(ctypes.Structure):
+    _fields_ = [("pages", _c_p), ("n_pages", _i32), ("heads", _i32), ("dim", _i32), ("page", _i32), ("group", _i32),
+                ("flags", _u32), ("device", _i32)]
+
+
+class _KvTable(ctypes.Structure):
+    _fields_ = [("pages", _c_p), ("row_stride", _i64), ("batch", _i32), ("width", _i32)]
+
+
+_CACHE_P, _TABLE_P = ctypes.POINTER(_KvCache), ctypes.POINTER(_KvTable)
+
 _SIGNATURES = {
     "stagq_side_record_count": (_i64, [_i32, _i32, _dbl]),
     "stagq_encode": (ctypes.c_int, [_c_p, _dbl, _i32, _i32, ctypes.POINTER(_Fields)]),
@@ -83,6 +100,18 @@ _SIGNATURES = {
     "stagq_check": (ctypes.c_int, [_c_p]),
     "stagq_debug_stall": (ctypes.c_int, [_c_p, _u32]),
     "stagq_debug_side_record": (ctypes.c_int, [_c_p, ctypes.POINTER(_SideLayout), _c_p, _i64, _c_p, _i64]),
+    "stagq_i8_row_bytes": (_i64, [_i32]),
+    "stagq_quantize_i8": (ctypes.c_int, [_c_p, _i64, _i32, _i32, _u32, _c_p, _c_p, ctypes.c_int, _c_p]),
+    "stagq_gemm_i8": (ctypes.c_int, [_c_p, _c_p, _i32, _c_p, _c_p, _i32, _i32, _c_p, _i64, _u32, ctypes.c_int, _c_p]),
+    "stagq_kv_page_bytes": (_i64, [_CACHE_P]),
+    "stagq_kv_append": (ctypes.c_int, [_CACHE_P, _TABLE_P, _c_p, _c_p, _i64, _c_p, _i64, _i32, _c_p]),
+    "stagq_kv_read": (ctypes.c_int, [_CACHE_P, _TABLE_P, _c_p, _c_p, _c_p, _i64, _c_p, _i64, _i32, _u32, _c_p]),
+    "stagq_kv_attention": (ctypes.c_int, [_CACHE_P, _TABLE_P, _c_p, _i32, _c_p, _i64, _i32, _i32, ctypes.c_float, _c_p,
+                                          _i64, _c_p, _i64, _i64, _c_p, _i64, _c_p]),
+    "stagq_kv_attention_workspace": (_i64, [_CACHE_P, _i32, _i32, _i32, _i32, ctypes.c_int]),
+    "stagq_kv_evict": (ctypes.c_int, [_CACHE_P, _TABLE_P, _c_p, _i32, _c_p, _i64, _i64, _i32, _i32, _TABLE_P, _c_p, _c_p,
+                                      _c_p, _i64, _i64, _i32, _c_p]),
+    "stagq_ops_check": (ctypes.c_int, [ctypes.c_int]),
     "stagq_free": (None, [_c_p]),
     "stagq_strerror": (ctypes.c_char_p, [ctypes.c_int]),
     "stagq_last_error": (ctypes.c_char_p, []),
@@ -462,3 +491,259 @@ def stagq_debug_side_record(m: Matrix):
 
 def stagq_free(m: Matrix) -> None:
     m.free()
+
+
+# ------------------------------------------------------- operators beside the GEMV
+
+_SIXTEEN = ("float16", "bfloat16")
+
+
+def _op_stream(stream, device: int) -> int:
+    """The stream of a call on `device`: the given one, else torch's current one there."""
+    if stream is None:
+        import torch
+        return torch.cuda.current_stream(device).cuda_stream
+    return getattr(stream, "cuda_stream", stream)
+
+
+def _check_op(t, name: str, dtypes, device: int) -> str:
+    """The name of t's dtype, one of `dtypes`; t is a CUDA tensor of `device`."""
+    import torch
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch tensor")
+    dtype = str(t.dtype)[6:]
+    if dtype not in dtypes:
+        raise TypeError(f"{name} must be {' or '.join(dtypes)}, got {dtype}")
+    if not t.is_cuda or t.get_device() != device:
+        raise ValueError(f"{name} must be on cuda:{device} (the call's GPU), got {t.device}")
+    return dtype
+
+
+def _check_rows(t, name: str, rows: int, cols: int, dtypes, device: int) -> str:
+    """t is [rows, cols] with unit stride along a row; rows may lie further apart."""
+    dtype = _check_op(t, name, dtypes, device)
+    if t.dim() != 2 or t.shape[0] != rows or t.shape[1] != cols:
+        raise ValueError(f"{name} must be [{rows}, {cols}], got {list(t.shape)}")
+    if (cols > 1 and t.stride(1) != 1) or (rows > 1 and t.stride(0) < cols):
+        raise ValueError(f"{name} must have unit stride along its rows, which must not overlap")
+    return dtype
+
+
+def _row_stride(t) -> int:
+    """Elements between the rows of a checked [rows, cols] tensor (a single row's own length)."""
+    return t.stride(0) if t.shape[0] > 1 else t.shape[1]
+
+
+def _check_flat(t, name: str, shape, dtype: str, device: int) -> None:
+    _check_op(t, name, (dtype,), device)
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+
+
+def _cuda_index(t, name: str) -> int:
+    import torch
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch tensor")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be on a GPU, got {t.device}")
+    return t.get_device()
+
+
+def stagq_i8_row_bytes(inp: int) -> int:
+    """Bytes of a row of `inp` 8-bit values: rows are padded with zeros to 128 bytes."""
+    n = int(lib().stagq_i8_row_bytes(inp))
+    if n < 0:
+        raise ValueError("inp outside 1..STAGQ_MAX_IN")
+    return n
+
+
+def stagq_quantize_i8(x, q, scale, stream=None) -> None:
+    """Rows of x [n, inp] (fp16 or bf16) rounded to 8 bits: q int8 [n,
+    stagq_i8_row_bytes(inp)], scale fp32 [n]. Serves tokens and, once, the
+    rows of a weight matrix (its output channels)."""
+    dev = _cuda_index(x, "x")
+    if x.dim() != 2:
+        raise ValueError(f"x must be [n, inp], got {list(x.shape)}")
+    n, inp = x.shape
+    dtype = _check_rows(x, "x", n, inp, _SIXTEEN, dev)
+    _check_flat(q, "q", (n, stagq_i8_row_bytes(inp)), "int8", dev)
+    _check_flat(scale, "scale", (n,), "float32", dev)
+    _check(lib().stagq_quantize_i8(x.data_ptr(), _row_stride(x), n, inp, STAGQ_BF16 if dtype == "bfloat16" else 0,
+                                   q.data_ptr(), scale.data_ptr(), dev, _op_stream(stream, dev)), "stagq_quantize_i8")
+
+
+def stagq_gemm_i8(xq, xscale, wq, wscale, inp: int, y, stream=None) -> None:
+    """y[i, j] = xscale[i] wscale[j] sum_k xq[i, k] wq[j, k] over k < inp:
+    xq int8 [n, row bytes] and wq int8 [out, row bytes] as stagq_quantize_i8
+    leaves them, y [n, out] in fp16, bf16 or fp32."""
+    dev = _cuda_index(xq, "xq")
+    n, out, row = xq.shape[0], wq.shape[0], stagq_i8_row_bytes(inp)
+    _check_flat(xq, "xq", (n, row), "int8", dev)
+    _check_flat(wq, "wq", (out, row), "int8", dev)
+    _check_flat(xscale, "xscale", (n,), "float32", dev)
+    _check_flat(wscale, "wscale", (out,), "float32", dev)
+    dtype = _check_rows(y, "y", n, out, ("float16", "bfloat16", "float32"), dev)
+    flags = STAGQ_Y_F32 if dtype == "float32" else STAGQ_BF16 if dtype == "bfloat16" else 0
+    _check(lib().stagq_gemm_i8(xq.data_ptr(), xscale.data_ptr(), n, wq.data_ptr(), wscale.data_ptr(), out, inp,
+                               y.data_ptr(), _row_stride(y), flags, dev, _op_stream(stream, dev)), "stagq_gemm_i8")
+
+
+def stagq_kv_page_bytes(heads: int, dim: int, page: int, group: int) -> int:
+    """Bytes of one page of a 4-bit cache."""
+    n = int(lib().stagq_kv_page_bytes(ctypes.byref(_KvCache(None, 1, heads, dim, page, group, 0, 0))))
+    if n < 0:
+        raise ValueError(f"no such cache: {lib().stagq_last_error().decode()}")
+    return n
+
+
+class KVCache:
+    """A pool of pages of a 4-bit K and V cache (the tensor `pages`, uint8,
+    stays the caller's): dim 64 or 128, `page` tokens a power of two from 16,
+    groups of 32, 64 or 128 channels, fp16 or bf16."""
+
+    def __init__(self, pages, heads: int, dim: int, page: int, group: int, dtype):
+        self.page_bytes = stagq_kv_page_bytes(heads, dim, page, group)
+        self.device = _cuda_index(pages, "pages")
+        _check_op(pages, "pages", ("uint8",), self.device)
+        if not pages.is_contiguous():
+            raise ValueError("pages must be contiguous")
+        if pages.numel() < self.page_bytes or pages.numel() % self.page_bytes:
+            raise ValueError(f"pages holds {pages.numel()} bytes, not a multiple of a page's {self.page_bytes}")
+        self.dtype = str(dtype)[6:]
+        if self.dtype not in _SIXTEEN:
+            raise TypeError(f"a cache is float16 or bfloat16, got {dtype}")
+        self.pages, self.heads, self.dim, self.page, self.group = pages, heads, dim, page, group
+        self._c = _KvCache(pages.data_ptr(), pages.numel() // self.page_bytes, heads, dim, page, group,
+                           STAGQ_BF16 if self.dtype == "bfloat16" else 0, self.device)
+
+    def _table(self, table, name: str = "table") -> _KvTable:
+        _check_op(table, name, ("int32",), self.device)
+        if table.dim() != 2 or 0 in table.shape or (table.shape[1] > 1 and table.stride(1) != 1) or \
+                (table.shape[0] > 1 and table.stride(0) < table.shape[1]):
+            raise ValueError(f"{name} must be [batch, pages of a sequence] with unit stride along its rows")
+        return _KvTable(table.data_ptr(), _row_stride(table), table.shape[0], table.shape[1])
+
+    def _mass(self, mass, name: str, batch: int):
+        _check_op(mass, name, ("float32",), self.device)
+        if mass.dim() != 3 or tuple(mass.shape[:2]) != (batch, self.heads) or mass.shape[2] < 1 or \
+                (mass.shape[2] > 1 and mass.stride(2) != 1):
+            raise ValueError(f"{name} must be [{batch}, {self.heads}, tokens] with unit stride along the tokens")
+        rows = mass.stride(1) if self.heads > 1 else mass.shape[2]
+        return (mass.stride(0) if batch > 1 else rows * self.heads), rows
+
+
+def stagq_kv_append(cache: KVCache, k, v, table, starts, n: int, stream=None) -> None:
+    """Rounds n new tokens of every sequence to 4 bits and writes them from
+    position starts[b] on (a negative start: nothing). k, v: [batch * n,
+    heads * dim]; table int32 [batch, pages]; starts int32 [batch]."""
+    t = cache._table(table)
+    cols = cache.heads * cache.dim
+    _check_rows(k, "k", t.batch * n, cols, (cache.dtype,), cache.device)
+    _check_rows(v, "v", t.batch * n, cols, (cache.dtype,), cache.device)
+    _check_flat(starts, "starts", (t.batch,), "int32", cache.device)
+    _check(lib().stagq_kv_append(cache._c, t, starts.data_ptr(), k.data_ptr(), _row_stride(k), v.data_ptr(),
+                                 _row_stride(v), n, _op_stream(stream, cache.device)), "stagq_kv_append")
+
+
+def stagq_kv_read(cache: KVCache, table, lens, k, v, n: int, starts=None, stream=None) -> None:
+    """The cached values of positions starts[b] .. starts[b] + n - 1 (no
+    starts: from 0) as rows of k and v [batch * n, heads * dim], in the
+    cache's type or fp32; zeros from lens[b] on (no lens: no bound)."""
+    t = cache._table(table)
+    cols = cache.heads * cache.dim
+    dtype = _check_rows(k, "k", t.batch * n, cols, (cache.dtype, "float32"), cache.device)
+    _check_rows(v, "v", t.batch * n, cols, (dtype,), cache.device)
+    for x, name in ((starts, "starts"), (lens, "lens")):
+        if x is not None:
+            _check_flat(x, name, (t.batch,), "int32", cache.device)
+    _check(lib().stagq_kv_read(cache._c, t, None if starts is None else starts.data_ptr(),
+                               None if lens is None else lens.data_ptr(), k.data_ptr(), _row_stride(k), v.data_ptr(),
+                               _row_stride(v), n, STAGQ_Y_F32 if dtype == "float32" else 0,
+                               _op_stream(stream, cache.device)), "stagq_kv_read")
+
+
+def stagq_kv_attention_workspace(cache: KVCache, batch: int, max_len: int, q_heads: int, n_new: int = 1,
+                                 tracked: bool = False) -> int:
+    """Workspace bytes of a stagq_kv_attention call (`tracked`: with a mass)."""
+    n = int(lib().stagq_kv_attention_workspace(cache._c, batch, max_len, q_heads, n_new, int(tracked)))
+    if n < 0:
+        raise ValueError(f"stagq_kv_attention_workspace: {lib().stagq_last_error().decode()}")
+    return n
+
+
+def stagq_kv_attention(cache: KVCache, q, table, lens, out, n_new: int = 1, scale=None, mass=None, max_len=None,
+                       workspace=None, stream=None) -> None:
+    """Attention of the n_new newest tokens of every sequence over its cache.
+    q, out: [batch * n_new, q_heads * dim]; lens int32 [batch], cached tokens
+    with the new ones; scale: 1 / sqrt(dim) unless given; mass fp32 [batch,
+    heads, tokens]: adds every token's weights to it. max_len (a bound on
+    lens) defaults to what the table, and the mass, hold. workspace: a uint8
+    tensor of stagq_kv_attention_workspace bytes, else one is allocated."""
+    t = cache._table(table)
+    dev = cache.device
+    rows = t.batch * n_new
+    _check_op(q, "q", (cache.dtype,), dev)
+    if q.dim() != 2 or q.shape[1] == 0 or q.shape[1] % cache.dim:
+        raise ValueError(f"q must be [{rows}, q_heads * {cache.dim}], got {list(q.shape)}")
+    _check_rows(q, "q", rows, q.shape[1], (cache.dtype,), dev)
+    _check_rows(out, "out", rows, q.shape[1], (cache.dtype,), dev)
+    _check_flat(lens, "lens", (t.batch,), "int32", dev)
+    q_heads = q.shape[1] // cache.dim
+    mb = mh = 0
+    cap = t.width * cache.page
+    if mass is not None:
+        mb, mh = cache._mass(mass, "mass", t.batch)
+        cap = min(cap, mass.shape[2])
+    if max_len is None:
+        max_len = cap
+    elif max_len > cap:
+        raise ValueError(f"max_len {max_len} exceeds the {cap} tokens of the table and the mass")
+    s = _op_stream(stream, dev)
+    need = stagq_kv_attention_workspace(cache, t.batch, max_len, q_heads, n_new, mass is not None)
+    if workspace is not None:
+        _check_op(workspace, "workspace", ("uint8",), dev)
+        if not workspace.is_contiguous():
+            raise ValueError("workspace must be contiguous")
+    elif need:
+        import torch
+        workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+        if stream is not None:  # the allocator must not reuse it while `stream` still does
+            workspace.record_stream(torch.cuda.ExternalStream(s, device=dev))
+    _check(lib().stagq_kv_attention(cache._c, t, lens.data_ptr(), max_len, q.data_ptr(), _row_stride(q), q_heads, n_new,
+                                    cache.dim ** -0.5 if scale is None else scale, out.data_ptr(), _row_stride(out),
+                                    None if mass is None else mass.data_ptr(), mb, mh,
+                                    None if workspace is None else workspace.data_ptr(),
+                                    0 if workspace is None else workspace.numel(), s), "stagq_kv_attention")
+
+
+def stagq_kv_evict(cache: KVCache, table, lens, mass, fresh, budget: int, recent: int, kept, new_lens, new_mass,
+                   max_len=None, stream=None) -> None:
+    """Thins every sequence out to `budget` tokens per KV head: its last
+    `recent` ones and those of the largest mass, copied in their order to the
+    pages of `fresh` (none of table's). kept int32 [batch, heads, budget];
+    new_lens int32 [batch]; new_mass fp32 [batch, heads, >= budget]."""
+    t, f = cache._table(table), cache._table(fresh, "fresh")
+    dev = cache.device
+    if f.batch != t.batch:
+        raise ValueError("the two tables differ in batch")
+    _check_flat(lens, "lens", (t.batch,), "int32", dev)
+    mb, mh = cache._mass(mass, "mass", t.batch)
+    nb, nh = cache._mass(new_mass, "new_mass", t.batch)
+    _check_flat(kept, "kept", (t.batch, cache.heads, budget), "int32", dev)
+    _check_flat(new_lens, "new_lens", (t.batch,), "int32", dev)
+    cap = min(t.width * cache.page, mass.shape[2])
+    if max_len is None:
+        max_len = cap
+    elif max_len > cap:
+        raise ValueError(f"max_len {max_len} exceeds the {cap} tokens of the table and the mass")
+    _check(lib().stagq_kv_evict(cache._c, t, lens.data_ptr(), max_len, mass.data_ptr(), mb, mh, budget, recent, f,
+                                kept.data_ptr(), new_lens.data_ptr(), new_mass.data_ptr(), nb, nh, new_mass.shape[2],
+                                _op_stream(stream, dev)), "stagq_kv_evict")
+
+
+def stagq_ops_check(device: int = 0) -> None:
+    """Waits for the device and raises on what the operators' kernels noted: a
+    page number, position or length out of bounds, or a wait that ran out."""
+    _check(lib().stagq_ops_check(device), "stagq_ops_check")

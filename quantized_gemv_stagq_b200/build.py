@@ -14,8 +14,10 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libstagq.so")
 
-SOURCES = ["api.cu", "gemv.cu", "gemv1.cu", "encoder.cpp", "stream.cpp"]
-HEADERS = ["layout.cuh", "kernel_common.cuh", "device_matrix.hpp", "host_common.hpp", "stream.hpp"]
+SOURCES = ["api.cu", "gemv.cu", "gemv1.cu", "encoder.cpp", "stream.cpp",
+           "ops_api.cu", "gemm_i8.cu", "kv_cache.cu", "kv_attention.cu"]
+HEADERS = ["layout.cuh", "kernel_common.cuh", "device_matrix.hpp", "host_common.hpp", "stream.hpp",
+           "ops_common.cuh", "gemm_i8.hpp", "kv_cache.hpp"]
 
 NVCC_FLAGS = [
     "-gencode", "arch=compute_100a,code=sm_100a",

@@ -1,0 +1,77 @@
+// Arguments of the 4-bit cache's kernels, and their launchers.
+#pragma once
+#include <cuda_runtime.h>
+
+#include <cstdint>
+
+#include "stagq.h"
+
+namespace stagq {
+
+// The pool and one call's page table. A (page, head, K | V) block holds
+// `page` rows of dim / 2 code bytes, then `page` rows of dim / group pairs
+// (scale, lowest) of the cache's 16-bit type.
+struct KvView {
+  uint8_t* pages;
+  const int32_t* table;
+  int64_t table_stride;    // entries between the table rows of two sequences
+  int64_t page_stride;     // bytes of a page (all heads, K and V)
+  int32_t block_bytes;     // bytes of a (page, head, K | V) block
+  int32_t n_pages, table_width, heads, dim, group, page, page_shift;
+  int32_t bf16;
+};
+
+struct KvRowsArgs {        // append and read
+  KvView kv;
+  void* k;                 // 16-bit rows (fp32 for a read with STAGQ_Y_F32)
+  void* v;
+  int64_t k_stride, v_stride;  // elements between two rows
+  const int32_t* starts;   // null: 0
+  const int32_t* lens;     // read only; null: no bound
+  int64_t n_rows;          // batch * n
+  int32_t n, f32, vec;     // tokens per sequence; fp32 output; 16-byte accesses allowed
+};
+
+struct KvAttnArgs {
+  KvView kv;
+  const uint16_t* q;
+  uint16_t* out;
+  int64_t q_stride, out_stride;
+  const int32_t* lens;
+  float* mass;             // null: not tracked
+  int64_t mass_stride_b, mass_stride_h;
+  float* part_o;           // [batch * heads * rows_pad][splits][dim]
+  float2* part_ml;         // [batch * heads * rows_pad][splits]
+  float* scores;           // [batch * heads][rows_pad][score_stride]
+  int64_t score_stride;
+  int32_t batch, q_heads, per, n_new, rows, rows_pad, row_blocks, splits, max_len, vec;
+  float scale_log2;        // softmax scale times log2(e)
+};
+
+struct KvEvictArgs {
+  KvView src, dst;
+  const int32_t* lens;
+  const float* mass;
+  float* new_mass;
+  int32_t* kept;
+  int32_t* new_lens;
+  int64_t mass_stride_b, mass_stride_h, new_mass_stride_b, new_mass_stride_h;
+  int32_t batch, max_len, budget, recent, new_cap;
+};
+
+struct KvAttnPlan {
+  int nt;                  // query rows per CTA: 4 * nt
+  int row_blocks, splits, rows_pad;
+  int64_t score_stride;
+  int64_t off_ml, off_o, off_scores, bytes;  // workspace layout
+};
+
+KvAttnPlan plan_kv_attention(int batch, int heads, int q_heads, int n_new, int dim, int max_len, bool mass,
+                             int num_sms);
+
+cudaError_t launch_kv_append(const KvRowsArgs& a, cudaStream_t s);
+cudaError_t launch_kv_read(const KvRowsArgs& a, cudaStream_t s);
+cudaError_t launch_kv_attention(const KvAttnArgs& a, const KvAttnPlan& p, cudaStream_t s);
+cudaError_t launch_kv_evict(const KvEvictArgs& a, cudaStream_t s);
+
+}  // namespace stagq
