@@ -10,10 +10,12 @@
 // Bound by the cache's bytes as long as the unpacking keeps up: at 6.5 TB/s an
 // SM takes in about 49 codes per clock. What keeps the instruction count near
 // one per two codes:
-//  - A code masked out of its word, in place, IS an fp16 number: 4 bits at the
-//    bottom of a half are the subnormal u 2^-24, 4 bits above them 16 u 2^-24.
-//    Both are exact, mma multiplies subnormals at full rate, and the 16 and
-//    2^24 go into q and the scales. One AND gives two operands.
+//  - Two codes are masked out of a word in place and OR'ed under the exponent
+//    of 1024 in one operation; a packed subtraction leaves u - 8 (16 times that
+//    for the upper 4 bits of a byte) as exact fp16, and lo + 8 s replaces lo.
+//    Without the subtraction the masked bits are fp16 subnormals, exact too, and
+//    mma takes them: but it aligns products by their nominal exponents, and the
+//    result was 2e-4 off at 67000 tokens (fp16 rounds by 2e-4), now 2e-7.
 //  - The order of a contraction is free, so the packed order of a row is the
 //    order of the mma fragments (kv_cache.cu): a lane's K words feed its
 //    A fragments without a shuffle, and two tokens' V words give the pairs of
