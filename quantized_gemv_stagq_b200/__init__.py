@@ -10,6 +10,7 @@ there is no fallback implementation.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 from dataclasses import dataclass
 
@@ -495,60 +496,75 @@ def stagq_free(m: Matrix) -> None:
 
 # ------------------------------------------------------- operators beside the GEMV
 
+# A call of these operators takes microseconds on the GPU, so the checks below
+# look at each tensor once and the shapes of a cache are checked when it is made.
+
 _SIXTEEN = ("float16", "bfloat16")
+_tensor_type = None
+_dtype_names = {}
+_raw_stream = None
+
+
+def _torch_names() -> None:
+    """Binds what the checks need of torch, on the first call of an operator."""
+    global _tensor_type, _raw_stream
+    import torch
+    for name in ("float16", "bfloat16", "float32", "int8", "uint8", "int32"):
+        _dtype_names[getattr(torch, name)] = name
+    _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
+        (lambda device: torch.cuda.current_stream(device).cuda_stream)
+    _tensor_type = torch.Tensor
 
 
 def _op_stream(stream, device: int) -> int:
     """The stream of a call on `device`: the given one, else torch's current one there."""
     if stream is None:
-        import torch
-        return torch.cuda.current_stream(device).cuda_stream
+        return _raw_stream(device)
     return getattr(stream, "cuda_stream", stream)
+
+
+def _cuda_index(t, name: str) -> int:
+    if _tensor_type is None:
+        _torch_names()
+    if not isinstance(t, _tensor_type):
+        raise TypeError(f"{name} must be a torch tensor")
+    device = t.get_device()
+    if device < 0 or not t.is_cuda:
+        raise ValueError(f"{name} must be on a GPU, got {t.device}")
+    return device
 
 
 def _check_op(t, name: str, dtypes, device: int) -> str:
     """The name of t's dtype, one of `dtypes`; t is a CUDA tensor of `device`."""
-    import torch
-    if not isinstance(t, torch.Tensor):
+    if not isinstance(t, _tensor_type):
         raise TypeError(f"{name} must be a torch tensor")
-    dtype = str(t.dtype)[6:]
+    dtype = _dtype_names.get(t.dtype)
     if dtype not in dtypes:
-        raise TypeError(f"{name} must be {' or '.join(dtypes)}, got {dtype}")
-    if not t.is_cuda or t.get_device() != device:
+        raise TypeError(f"{name} must be {' or '.join(dtypes)}, got {t.dtype}")
+    if t.get_device() != device:
         raise ValueError(f"{name} must be on cuda:{device} (the call's GPU), got {t.device}")
     return dtype
 
 
-def _check_rows(t, name: str, rows: int, cols: int, dtypes, device: int) -> str:
-    """t is [rows, cols] with unit stride along a row; rows may lie further apart."""
+def _check_rows(t, name: str, rows: int, cols: int, dtypes, device: int):
+    """t is [rows, cols] with unit stride along a row; rows may lie further
+    apart. Returns the name of its dtype and the elements between two rows (a
+    single row's own length)."""
     dtype = _check_op(t, name, dtypes, device)
-    if t.dim() != 2 or t.shape[0] != rows or t.shape[1] != cols:
+    if tuple(t.shape) != (rows, cols):
         raise ValueError(f"{name} must be [{rows}, {cols}], got {list(t.shape)}")
-    if (cols > 1 and t.stride(1) != 1) or (rows > 1 and t.stride(0) < cols):
+    row, col = t.stride()
+    if (cols > 1 and col != 1) or (rows > 1 and row < cols):
         raise ValueError(f"{name} must have unit stride along its rows, which must not overlap")
-    return dtype
-
-
-def _row_stride(t) -> int:
-    """Elements between the rows of a checked [rows, cols] tensor (a single row's own length)."""
-    return t.stride(0) if t.shape[0] > 1 else t.shape[1]
+    return dtype, row if rows > 1 else cols
 
 
 def _check_flat(t, name: str, shape, dtype: str, device: int) -> None:
     _check_op(t, name, (dtype,), device)
-    if tuple(t.shape) != tuple(shape):
+    if tuple(t.shape) != shape:
         raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
-
-
-def _cuda_index(t, name: str) -> int:
-    import torch
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{name} must be a torch tensor")
-    if not t.is_cuda:
-        raise ValueError(f"{name} must be on a GPU, got {t.device}")
-    return t.get_device()
 
 
 def stagq_i8_row_bytes(inp: int) -> int:
@@ -567,10 +583,10 @@ def stagq_quantize_i8(x, q, scale, stream=None) -> None:
     if x.dim() != 2:
         raise ValueError(f"x must be [n, inp], got {list(x.shape)}")
     n, inp = x.shape
-    dtype = _check_rows(x, "x", n, inp, _SIXTEEN, dev)
+    dtype, stride = _check_rows(x, "x", n, inp, _SIXTEEN, dev)
     _check_flat(q, "q", (n, stagq_i8_row_bytes(inp)), "int8", dev)
     _check_flat(scale, "scale", (n,), "float32", dev)
-    _check(lib().stagq_quantize_i8(x.data_ptr(), _row_stride(x), n, inp, STAGQ_BF16 if dtype == "bfloat16" else 0,
+    _check(lib().stagq_quantize_i8(x.data_ptr(), stride, n, inp, STAGQ_BF16 if dtype == "bfloat16" else 0,
                                    q.data_ptr(), scale.data_ptr(), dev, _op_stream(stream, dev)), "stagq_quantize_i8")
 
 
@@ -584,12 +600,13 @@ def stagq_gemm_i8(xq, xscale, wq, wscale, inp: int, y, stream=None) -> None:
     _check_flat(wq, "wq", (out, row), "int8", dev)
     _check_flat(xscale, "xscale", (n,), "float32", dev)
     _check_flat(wscale, "wscale", (out,), "float32", dev)
-    dtype = _check_rows(y, "y", n, out, ("float16", "bfloat16", "float32"), dev)
+    dtype, stride = _check_rows(y, "y", n, out, ("float16", "bfloat16", "float32"), dev)
     flags = STAGQ_Y_F32 if dtype == "float32" else STAGQ_BF16 if dtype == "bfloat16" else 0
     _check(lib().stagq_gemm_i8(xq.data_ptr(), xscale.data_ptr(), n, wq.data_ptr(), wscale.data_ptr(), out, inp,
-                               y.data_ptr(), _row_stride(y), flags, dev, _op_stream(stream, dev)), "stagq_gemm_i8")
+                               y.data_ptr(), stride, flags, dev, _op_stream(stream, dev)), "stagq_gemm_i8")
 
 
+@functools.lru_cache(maxsize=None)
 def stagq_kv_page_bytes(heads: int, dim: int, page: int, group: int) -> int:
     """Bytes of one page of a 4-bit cache."""
     n = int(lib().stagq_kv_page_bytes(ctypes.byref(_KvCache(None, 1, heads, dim, page, group, 0, 0))))
@@ -611,19 +628,23 @@ class KVCache:
             raise ValueError("pages must be contiguous")
         if pages.numel() < self.page_bytes or pages.numel() % self.page_bytes:
             raise ValueError(f"pages holds {pages.numel()} bytes, not a multiple of a page's {self.page_bytes}")
-        self.dtype = str(dtype)[6:]
+        self.dtype = _dtype_names.get(dtype)
         if self.dtype not in _SIXTEEN:
             raise TypeError(f"a cache is float16 or bfloat16, got {dtype}")
         self.pages, self.heads, self.dim, self.page, self.group = pages, heads, dim, page, group
+        self._types = (self.dtype,)
+        self._row = heads * dim
         self._c = _KvCache(pages.data_ptr(), pages.numel() // self.page_bytes, heads, dim, page, group,
                            STAGQ_BF16 if self.dtype == "bfloat16" else 0, self.device)
 
     def _table(self, table, name: str = "table") -> _KvTable:
         _check_op(table, name, ("int32",), self.device)
-        if table.dim() != 2 or 0 in table.shape or (table.shape[1] > 1 and table.stride(1) != 1) or \
-                (table.shape[0] > 1 and table.stride(0) < table.shape[1]):
-            raise ValueError(f"{name} must be [batch, pages of a sequence] with unit stride along its rows")
-        return _KvTable(table.data_ptr(), _row_stride(table), table.shape[0], table.shape[1])
+        if table.dim() != 2 or 0 in table.shape:
+            raise ValueError(f"{name} must be [batch, pages of a sequence], got {list(table.shape)}")
+        (batch, width), (row, col) = table.shape, table.stride()
+        if (width > 1 and col != 1) or (batch > 1 and row < width):
+            raise ValueError(f"{name} must have unit stride along its rows, which must not overlap")
+        return _KvTable(table.data_ptr(), row if batch > 1 else width, batch, width)
 
     def _mass(self, mass, name: str, batch: int):
         _check_op(mass, name, ("float32",), self.device)
@@ -638,30 +659,28 @@ def stagq_kv_append(cache: KVCache, k, v, table, starts, n: int, stream=None) ->
     """Rounds n new tokens of every sequence to 4 bits and writes them from
     position starts[b] on (a negative start: nothing). k, v: [batch * n,
     heads * dim]; table int32 [batch, pages]; starts int32 [batch]."""
-    t = cache._table(table)
-    cols = cache.heads * cache.dim
-    _check_rows(k, "k", t.batch * n, cols, (cache.dtype,), cache.device)
-    _check_rows(v, "v", t.batch * n, cols, (cache.dtype,), cache.device)
-    _check_flat(starts, "starts", (t.batch,), "int32", cache.device)
-    _check(lib().stagq_kv_append(cache._c, t, starts.data_ptr(), k.data_ptr(), _row_stride(k), v.data_ptr(),
-                                 _row_stride(v), n, _op_stream(stream, cache.device)), "stagq_kv_append")
+    t, dev = cache._table(table), cache.device
+    _, ks = _check_rows(k, "k", t.batch * n, cache._row, cache._types, dev)
+    _, vs = _check_rows(v, "v", t.batch * n, cache._row, cache._types, dev)
+    _check_flat(starts, "starts", (t.batch,), "int32", dev)
+    _check(lib().stagq_kv_append(cache._c, t, starts.data_ptr(), k.data_ptr(), ks, v.data_ptr(), vs, n,
+                                 _op_stream(stream, dev)), "stagq_kv_append")
 
 
 def stagq_kv_read(cache: KVCache, table, lens, k, v, n: int, starts=None, stream=None) -> None:
     """The cached values of positions starts[b] .. starts[b] + n - 1 (no
     starts: from 0) as rows of k and v [batch * n, heads * dim], in the
     cache's type or fp32; zeros from lens[b] on (no lens: no bound)."""
-    t = cache._table(table)
-    cols = cache.heads * cache.dim
-    dtype = _check_rows(k, "k", t.batch * n, cols, (cache.dtype, "float32"), cache.device)
-    _check_rows(v, "v", t.batch * n, cols, (dtype,), cache.device)
-    for x, name in ((starts, "starts"), (lens, "lens")):
-        if x is not None:
-            _check_flat(x, name, (t.batch,), "int32", cache.device)
+    t, dev = cache._table(table), cache.device
+    dtype, ks = _check_rows(k, "k", t.batch * n, cache._row, (cache.dtype, "float32"), dev)
+    _, vs = _check_rows(v, "v", t.batch * n, cache._row, (dtype,), dev)
+    if starts is not None:
+        _check_flat(starts, "starts", (t.batch,), "int32", dev)
+    if lens is not None:
+        _check_flat(lens, "lens", (t.batch,), "int32", dev)
     _check(lib().stagq_kv_read(cache._c, t, None if starts is None else starts.data_ptr(),
-                               None if lens is None else lens.data_ptr(), k.data_ptr(), _row_stride(k), v.data_ptr(),
-                               _row_stride(v), n, STAGQ_Y_F32 if dtype == "float32" else 0,
-                               _op_stream(stream, cache.device)), "stagq_kv_read")
+                               None if lens is None else lens.data_ptr(), k.data_ptr(), ks, v.data_ptr(), vs, n,
+                               STAGQ_Y_F32 if dtype == "float32" else 0, _op_stream(stream, dev)), "stagq_kv_read")
 
 
 def stagq_kv_attention_workspace(cache: KVCache, batch: int, max_len: int, q_heads: int, n_new: int = 1,
@@ -684,13 +703,14 @@ def stagq_kv_attention(cache: KVCache, q, table, lens, out, n_new: int = 1, scal
     t = cache._table(table)
     dev = cache.device
     rows = t.batch * n_new
-    _check_op(q, "q", (cache.dtype,), dev)
-    if q.dim() != 2 or q.shape[1] == 0 or q.shape[1] % cache.dim:
+    _check_op(q, "q", cache._types, dev)
+    cols = q.shape[-1]
+    q_heads = cols // cache.dim
+    if cols == 0 or cols % cache.dim:
         raise ValueError(f"q must be [{rows}, q_heads * {cache.dim}], got {list(q.shape)}")
-    _check_rows(q, "q", rows, q.shape[1], (cache.dtype,), dev)
-    _check_rows(out, "out", rows, q.shape[1], (cache.dtype,), dev)
+    _, qs = _check_rows(q, "q", rows, cols, cache._types, dev)
+    _, outs = _check_rows(out, "out", rows, cols, cache._types, dev)
     _check_flat(lens, "lens", (t.batch,), "int32", dev)
-    q_heads = q.shape[1] // cache.dim
     mb = mh = 0
     cap = t.width * cache.page
     if mass is not None:
@@ -711,8 +731,8 @@ def stagq_kv_attention(cache: KVCache, q, table, lens, out, n_new: int = 1, scal
         workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
         if stream is not None:  # the allocator must not reuse it while `stream` still does
             workspace.record_stream(torch.cuda.ExternalStream(s, device=dev))
-    _check(lib().stagq_kv_attention(cache._c, t, lens.data_ptr(), max_len, q.data_ptr(), _row_stride(q), q_heads, n_new,
-                                    cache.dim ** -0.5 if scale is None else scale, out.data_ptr(), _row_stride(out),
+    _check(lib().stagq_kv_attention(cache._c, t, lens.data_ptr(), max_len, q.data_ptr(), qs, q_heads, n_new,
+                                    cache.dim ** -0.5 if scale is None else scale, out.data_ptr(), outs,
                                     None if mass is None else mass.data_ptr(), mb, mh,
                                     None if workspace is None else workspace.data_ptr(),
                                     0 if workspace is None else workspace.numel(), s), "stagq_kv_attention")

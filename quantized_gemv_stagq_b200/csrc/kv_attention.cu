@@ -30,11 +30,18 @@
 // shared memory first, 2 to 4 times the cache's bytes of shared-memory writes
 // and reads, for products that mma.sync does within the bytes' time.
 //
-// A warp takes 32 tokens at a time straight from global memory into registers
-// (the next 32 load while these are computed), the warps of a CTA take such
-// tiles in turn and join their sums once, at the end. Nothing in the loop
-// waits for another warp. Few (sequence, head) pairs are split over the
-// tokens; a second kernel joins the splits.
+// A warp takes 32 tokens at a time. Each has a ring of tiles in shared memory
+// of its own, filled by bulk copies (4 per tile, one per lane, 8 where a page
+// holds half a tile) two tiles ahead: no registers wait for memory, so 16 warps
+// fit an SM. The four warps of a CTA take tiles in turn and join their sums at
+// the end; nothing in the loop waits for another warp.
+//
+// The work is cut into rounds of 128 tokens (a tile per warp) of a unit
+// (sequence, KV head, block of query rows), numbered unit after unit, and every
+// CTA takes an equal run of that numbering, read off the lengths on the
+// device. A ragged batch, one long sequence and many short ones thus fill the
+// GPU alike. A unit that one CTA covers is written out; the others leave a
+// partial sum (at most two per CTA), and a second kernel joins those.
 #include <climits>
 
 #include "kernel_common.cuh"
@@ -52,7 +59,6 @@ using kernels::kFull;
 
 constexpr int kWarps = 4;
 constexpr int kTile = 32;            // tokens of a warp's tile
-constexpr int kMaxSplits = 256;
 
 __device__ __forceinline__ float ex2(float x) {
   float y;
@@ -72,11 +78,13 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t v) {
   return r;
 }
 // Two codes in their halves' lowest 4 bits (HIGH: the 4 above) as fp16 u - 8
-// (HIGH: 16 times that), exact: 0x6400 | u is the half 1024 + u.
+// (HIGH: 16 times that), exact: 0x6400 | u is the half 1024 + u. `exponent` is
+// 0x64006400 in a register: with two immediates the masking and the OR would
+// be two instructions.
 template <bool HIGH>
-__device__ __forceinline__ uint32_t centered(uint32_t w) {
-  const uint32_t v = (w & (HIGH ? 0x00F000F0u : 0x000F000Fu)) | 0x64006400u;
-  uint32_t r;
+__device__ __forceinline__ uint32_t centered(uint32_t w, uint32_t exponent) {
+  uint32_t v, r;
+  asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(v) : "r"(w), "n"(HIGH ? 0x00F000F0 : 0x000F000F), "r"(exponent));
   asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(v), "r"(HIGH ? 0x64806480u : 0x64086408u));
   return r;
 }
@@ -84,41 +92,57 @@ __device__ __forceinline__ uint32_t pack_half2(float lo, float hi) {
   const __half2 h = __floats2half2_rn(lo, hi);
   return *reinterpret_cast<const uint32_t*>(&h);
 }
+// Both values toward zero, hi in the upper half.
+__device__ __forceinline__ uint32_t pack_half2_rz(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rz.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+// The pair (scale, lowest) of a group.
+template <bool BF>
+__device__ __forceinline__ float pair_scale(uint32_t w) {
+  return BF ? __uint_as_float(w << 16) : __low2float(*reinterpret_cast<const __half2*>(&w));
+}
+template <bool BF>
+__device__ __forceinline__ float pair_low(uint32_t w) {
+  return BF ? __uint_as_float(w & 0xFFFF0000u) : __high2float(*reinterpret_cast<const __half2*>(&w));
+}
 // 2^e for -126 <= e <= 127.
 __device__ __forceinline__ float pow2(int e) { return __uint_as_float(static_cast<uint32_t>(e + 127) << 23); }
 
 template <int WORDS>
 __device__ __forceinline__ void load_words(uint32_t (&w)[WORDS], const uint8_t* p) {
-  static_assert(WORDS == 1 || WORDS == 2 || WORDS % 4 == 0, "one vector load, or several of 16 bytes");
+  static_assert(WORDS == 1 || WORDS == 2 || WORDS == 4, "one vector load");
   if constexpr (WORDS == 1) {
-    w[0] = __ldg(reinterpret_cast<const uint32_t*>(p));
+    w[0] = *reinterpret_cast<const uint32_t*>(p);
   } else if constexpr (WORDS == 2) {
-    const uint2 v = __ldg(reinterpret_cast<const uint2*>(p));
+    const uint2 v = *reinterpret_cast<const uint2*>(p);
     w[0] = v.x;
     w[1] = v.y;
   } else {
-#pragma unroll
-    for (int i = 0; i < WORDS / 4; ++i) {
-      const uint4 v = __ldg(reinterpret_cast<const uint4*>(p) + i);
-      w[4 * i] = v.x;
-      w[4 * i + 1] = v.y;
-      w[4 * i + 2] = v.z;
-      w[4 * i + 3] = v.w;
-    }
+    const uint4 v = *reinterpret_cast<const uint4*>(p);
+    w[0] = v.x;
+    w[1] = v.y;
+    w[2] = v.z;
+    w[3] = v.w;
   }
 }
 
-// One warp's 32 tokens as a lane (g = lane / 4, t = lane mod 4) holds them:
-// K codes of tokens 4 g .. 4 g + 3 (channels 32 j + 8 t + 0..7), V codes of
-// tokens 8 t .. 8 t + 7 (channels 32 j + 4 g + 0..3), and both pairs of
-// tokens 4 g .. 4 g + 3.
+constexpr int kStages = 3;
+constexpr uint64_t kWaitLimitNs = 2000000000ull;
+
+// A tile in shared memory: codes of K and of V (32 rows of D / 2 bytes each),
+// pairs of K and of V.
 template <int D, int NG>
-struct Tile {
-  uint32_t k[4][D / 32];
-  uint32_t v[8][D / 64];
-  uint32_t mk[4 * NG], mv[4 * NG];
-  bool ok;  // the page of tokens 4 g .. 4 g + 3 is in the pool
+struct TileLayout {
+  static constexpr int kCodes = kTile * D / 2, kPairs = kTile * 4 * NG;
+  static constexpr int kV = kCodes, kPairsK = 2 * kCodes, kPairsV = 2 * kCodes + kPairs;
+  static constexpr int kBytes = 2 * (kCodes + kPairs);
 };
+// Row r of a product's 16 (8 for each half) is token tau(r) of the tile's 16:
+// with 64-byte rows, the K rows that 8 lanes read at a time then lie in
+// different halves of the banks, and so do two of the four V rows.
+__device__ __forceinline__ int tau(int r) { return r ^ ((r >> 1) & 1); }
 
 // Query positions of row r: token r / per of the n_new newest sees the tokens
 // before `limit`.
@@ -131,34 +155,142 @@ __device__ __forceinline__ int clamped_len(const KvAttnArgs& a, int b) {
   return len < 0 ? 0 : min(len, a.max_len);
 }
 
-template <int D, int NG, int NT>
-__global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 3 : 2) kv_attention_kernel(const __grid_constant__ KvAttnArgs a) {
+// Rounds of 128 tokens of sequence b (one head, one block of query rows).
+__device__ __forceinline__ int rounds_of(const KvAttnArgs& a, int b) {
+  return (clamped_len(a, b) + kWarps * kTile - 1) / (kWarps * kTile);
+}
+// The rounds of the sequences before b, and of all of them. The lanes of a
+// warp take 32 sequences at a time.
+__device__ __forceinline__ int64_t rounds_before(const KvAttnArgs& a, int b, int lane) {
+  int64_t n = 0;
+  for (int i = lane; i < b; i += 32) n += rounds_of(a, i);
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) n += __shfl_xor_sync(kFull, n, d);
+  return n;
+}
+// CTAs that get a run of `total` rounds, of at least one round each, and the
+// first round of CTA c's.
+__device__ __forceinline__ int busy_ctas(int64_t total, int ctas) { return total < ctas ? static_cast<int>(total) : ctas; }
+__device__ __forceinline__ int64_t run_start(int64_t total, int c, int busy) { return total * c / busy; }
+
+template <int D, int NG, int NT, bool BF>
+__global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 4 : 2) kv_attention_kernel(const __grid_constant__ KvAttnArgs a) {
   constexpr int J = D / 32;       // blocks of 32 channels
   constexpr int JG = J / NG;      // blocks of a group
   constexpr int ROWS = 4 * NT;
-  __shared__ float s_o[kWarps][ROWS][D];
+  using L = TileLayout<D, NG>;
+  static_assert(kStages * L::kBytes >= ROWS * D * 4, "the warps' sums take the rings' place");
+  extern __shared__ __align__(128) uint8_t smem[];
   __shared__ float s_m[kWarps][ROWS], s_l[kWarps][ROWS];
+  __shared__ __align__(8) uint64_t s_full[kWarps][kStages];
+  __shared__ uint32_t s_ok[kWarps][kStages];  // by lane: whether its piece's page is in the pool
+  float (*s_o)[ROWS][D] = reinterpret_cast<float (*)[ROWS][D]>(smem);
 
   grid_launch_dependents();
   grid_dependency_wait();
   const KvView& kv = a.kv;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
-  int unit = blockIdx.x;
-  const int split = unit % a.splits;
-  unit /= a.splits;
-  const int rb = unit % a.row_blocks;
-  const int bh = unit / a.row_blocks;
-  const int b = bh / kv.heads, h = bh - b * kv.heads;
+  const int units_b = kv.heads * a.row_blocks;  // units of a sequence
+
+  uint8_t* ring = smem + warp * (kStages * L::kBytes);
+  const uint32_t ring_addr = kernels::smem_addr(ring), full_addr = kernels::smem_addr(&s_full[warp][0]);
+  if (lane < kStages) kernels::mbar_init(full_addr + 8 * lane, 1);
+  kernels::fence_barrier_init();
+  __syncthreads();
+  uint32_t filled = 0, used = 0;  // tiles that this warp has asked for, and waited for
+  bool dead = false;              // a wait ran out: nothing more is asked for or waited for
+  // What lane l copies of a tile: piece l / 4 of its tokens (two pieces where a
+  // page holds half a tile), K codes, V codes, K pairs or V pairs.
+  const int piece_tokens = min(kv.page, kTile), piece = kv.page < kTile ? (lane >> 2) & 1 : 0;
+  const int kind = lane & 3, row_bytes = kind < 2 ? D / 2 : 4 * NG;
+  const bool copies = lane < 4 * (kTile / piece_tokens);
+  const uint32_t copy_dst = (kind == 0 ? 0 : kind == 1 ? L::kV : kind == 2 ? L::kPairsK : L::kPairsV) +
+                            piece * piece_tokens * row_bytes;
+  const int copy_src = (kind & 1) * kv.block_bytes + (kind < 2 ? 0 : kv.page * (D / 2));
+  const int copy_bytes = piece_tokens * row_bytes;
+
+  for (int i = blockIdx.x; i < a.batch; i += gridDim.x) {  // sequences without a token have no unit
+    const int n = a.lens[i];
+    if (threadIdx.x == 0 && (n < 0 || n > a.max_len)) atomicOr(&g_status, kOpsBadPage);
+    if (n <= 0)
+      for (int c = threadIdx.x; c < a.n_new * a.q_heads * D; c += kWarps * 32) {
+        const int tok = c / (a.q_heads * D);
+        a.out[(static_cast<int64_t>(i) * a.n_new + tok) * a.out_stride + c - tok * a.q_heads * D] = 0;
+      }
+  }
+
+  // this CTA's run of rounds, and the sequence b that it starts in
+  const int64_t total = rounds_before(a, a.batch, lane) * units_b;
+  const int busy = busy_ctas(total, gridDim.x);
+  if (static_cast<int>(blockIdx.x) >= busy) return;
+  int64_t at = run_start(total, blockIdx.x, busy);
+  const int64_t run_end = run_start(total, blockIdx.x + 1, busy);
+  int b = 0;
+  int64_t before = 0;  // rounds before sequence b
+  for (int b0 = 0;; b0 += 32) {
+    const int64_t n = b0 + lane < a.batch ? static_cast<int64_t>(rounds_of(a, b0 + lane)) * units_b : 0;
+    int64_t sum = n;  // of this lane's sequence and those before it
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const int64_t o = __shfl_up_sync(kFull, sum, d);
+      if (lane >= d) sum += o;
+    }
+    const uint32_t past = __ballot_sync(kFull, before + sum > at);
+    if (past) {
+      const int l = __ffs(past) - 1;
+      b = b0 + l;
+      before += __shfl_sync(kFull, sum - n, l);
+      break;
+    }
+    before += __shfl_sync(kFull, sum, 31);
+  }
+  bool first_segment = true;
+  for (; at < run_end; first_segment = false) {
+  int rounds = rounds_of(a, b);
+  while (at >= before + static_cast<int64_t>(rounds) * units_b) {
+    before += static_cast<int64_t>(rounds) * units_b;
+    rounds = rounds_of(a, ++b);
+  }
+  const int unit = static_cast<int>((at - before) / rounds);  // of the sequence
+  const int round0 = static_cast<int>((at - before) - static_cast<int64_t>(unit) * rounds);
+  const int n_rounds = static_cast<int>(min(static_cast<int64_t>(rounds - round0), run_end - at));
+  at += n_rounds;
+  const int h = unit / a.row_blocks, rb = unit - h * a.row_blocks;
+  const int bh = b * kv.heads + h;
   const int r0 = rb * ROWS;
   const int len = clamped_len(a, b);
-  if (threadIdx.x == 0 && len != a.lens[b]) atomicOr(&g_status, kOpsBadPage);
   const int limmax = max(0, row_limit(a, len, min(r0 + ROWS, a.rows) - 1));  // of the block's last row
+  const int tile_end = min((limmax + kTile - 1) / kTile, (round0 + n_rounds) * kWarps);
+  int tile = round0 * kWarps + warp;
 
-  // this CTA's tiles: an even share of the sequence's, whole rounds of warps apart from the last
-  const int tiles = (limmax + kTile - 1) / kTile;
-  const int share = (tiles + a.splits - 1) / a.splits;
-  const int tile_end = min(tiles, (split + 1) * share);
-  int tile = split * share + warp;
+  const int last_page = max(0, (limmax - 1) >> kv.page_shift);
+  const int32_t* table = kv.table + b * kv.table_stride;
+  const uint8_t* head = kv.pages + static_cast<int64_t>(2 * h) * kv.block_bytes + copy_src;
+  // page number of the lane's piece of tile i (past the end: the last page)
+  auto page_of = [&](int i) { return __ldg(table + min((i * kTile + piece * piece_tokens) >> kv.page_shift, last_page)); };
+  auto ask = [&](int i, int pid) {
+    const int s = filled % kStages;
+    const bool ok = pid >= 0 && pid < kv.n_pages;
+    const uint32_t okm = __ballot_sync(kFull, ok);
+    if (lane == 0) {
+      s_ok[warp][s] = okm;
+      kernels::mbar_arrive_expect_tx(full_addr + 8 * s, L::kBytes);
+    }
+    __syncwarp();
+    if (copies)
+      kernels::bulk_load(ring_addr + s * L::kBytes + copy_dst,
+                         head + (ok ? pid : 0) * kv.page_stride + ((i * kTile + piece * piece_tokens) & (kv.page - 1)) * row_bytes,
+                         copy_bytes, full_addr + 8 * s);
+    ++filled;
+  };
+  int ahead = tile, pid = 0;  // the next tile to ask for, and its lane's page
+  if (ahead < tile_end) pid = page_of(ahead);
+  for (int i = 0; i < kStages - 1; ++i)
+    if (ahead < tile_end && !dead) {
+      ask(ahead, pid);
+      ahead += kWarps;
+      if (ahead < tile_end) pid = page_of(ahead);
+    }
 
   // q in fp16, each row scaled by a power of two so that its largest value is
   // in [2^10, 2^11): exact for fp16 and bf16 alike (and q / 16 too), down to
@@ -182,7 +314,7 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 3 : 2) kv_attention_ker
       }
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        x[j][i] = ops::load16(raw[i], kv.bf16);
+        x[j][i] = ops::load16(raw[i], BF);
         fine = fine && isfinite(x[j][i]);
         amax = fmaxf(amax, fabsf(x[j][i]));
       }
@@ -251,59 +383,49 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 3 : 2) kv_attention_ker
       for (int c = 0; c < 4; ++c) o[j][0][nt][c] = o[j][1][nt][c] = 0.0f;
   }
 
-  const int last_page = max(0, (limmax - 1) >> kv.page_shift);
-  const int32_t* table = kv.table + b * kv.table_stride;
-  const uint8_t* head = kv.pages + static_cast<int64_t>(2 * h) * kv.block_bytes;
-  const int meta_off = kv.page * (D / 2);
-  // page numbers of tile `i`'s tokens 4 g and 8 t (those past the end: the last page)
-  auto load_pages = [&](int i, int& pk, int& pv) {
-    pk = __ldg(table + min((i * kTile + 4 * g) >> kv.page_shift, last_page));
-    pv = __ldg(table + min((i * kTile + 8 * t) >> kv.page_shift, last_page));
-  };
-  auto load_tile = [&](int i, int pk, int pv, Tile<D, NG>& x) {
-    x.ok = pk >= 0 && pk < kv.n_pages;
-    pk = x.ok ? pk : 0;
-    pv = pv >= 0 && pv < kv.n_pages ? pv : 0;
-    const uint8_t* kb = head + pk * kv.page_stride;
-    const uint8_t* vb = head + pv * kv.page_stride + kv.block_bytes;
-    const int sk = (i * kTile + 4 * g) & (kv.page - 1), sv = (i * kTile + 8 * t) & (kv.page - 1);
-#pragma unroll
-    for (int n = 0; n < 4; ++n) load_words<J>(x.k[n], kb + (sk + n) * (D / 2) + t * (D / 8));
-    load_words<4 * NG>(x.mk, kb + meta_off + sk * (4 * NG));
-#pragma unroll
-    for (int n = 0; n < 8; ++n) load_words<J / 2>(x.v[n], vb + (sv + n) * (D / 2) + g * (D / 16));
-    load_words<4 * NG>(x.mv, head + pk * kv.page_stride + kv.block_bytes + meta_off + sk * (4 * NG));
-  };
-
-  Tile<D, NG> cur;
-  int pk = 0, pv = 0;
-  if (tile < tile_end) {
-    load_pages(tile, pk, pv);
-    load_tile(tile, pk, pv, cur);
-    if (tile + kWarps < tile_end) load_pages(tile + kWarps, pk, pv);
-  }
-  while (tile < tile_end) {
-    Tile<D, NG> nxt = cur;
-    const int next = tile + kWarps;
-    if (next < tile_end) {
-      load_tile(next, pk, pv, nxt);
-      if (next + kWarps < tile_end) load_pages(next + kWarps, pk, pv);
+  uint32_t exponent;
+  asm volatile("mov.b32 %0, 0x64006400;" : "=r"(exponent));
+  const uint32_t rest_mask = t < 2 ? 0u : 0xFFFFE000u;
+  const int tau_g = tau(g), tau_v = tau(2 * t), tau_w = tau(2 * t + 1);
+  for (; tile < tile_end && !dead; tile += kWarps) {
+    if (ahead < tile_end) {
+      ask(ahead, pid);
+      ahead += kWarps;
+      if (ahead < tile_end) pid = page_of(ahead);
     }
-    const int tok0 = tile * kTile + 4 * g;
-    const uint32_t bad = __ballot_sync(kFull, !cur.ok && tok0 < limmax);
+    const int stage = used % kStages;
+    dead = !__all_sync(kFull, kernels::mbar_wait(full_addr + 8 * stage, (used / kStages) & 1, kWaitLimitNs));
+    ++used;
+    if (dead) {
+      if (lane == 0) atomicOr(&g_status, kOpsTimeout);
+      for (; used < filled; ++used)  // the copies in flight land before the CTA goes
+        kernels::mbar_wait(full_addr + 8 * (used % kStages), (used / kStages) & 1, kWaitLimitNs);
+      break;
+    }
+    const uint8_t* x = ring + stage * L::kBytes;
+    const uint32_t okm = s_ok[warp][stage];
+    const int tok0 = tile * kTile + tau_g;  // this lane's tokens: tok0 + 8 n
+    const bool bad = okm != kFull;
     if (bad && lane == 0) atomicOr(&g_status, kOpsBadPage);
     const bool edge = (tile + 1) * kTile > lim_min || bad;  // some row does not see all of the tile
+    const bool ok[2] = {(okm & 1u) != 0, (okm & 16u) != 0};  // of the tile's first and last 16 tokens
+    uint32_t mk[4][NG], mv[4][NG];
+#pragma unroll
+    for (int n = 0; n < 4; ++n) {
+      load_words<NG>(mk[n], x + L::kPairsK + (tau_g + 8 * n) * (4 * NG));
+      load_words<NG>(mv[n], x + L::kPairsV + (tau_g + 8 * n) * (4 * NG));
+    }
     if (edge) {
       // tokens that no row sees may hold anything: their pairs count as zero
 #pragma unroll
       for (int n = 0; n < 4; ++n)
-        if (!cur.ok || tok0 + n >= limmax) {
+        if (!ok[n >> 1] || tok0 + 8 * n >= limmax) {
 #pragma unroll
-          for (int c = 0; c < NG; ++c) cur.mk[n * NG + c] = cur.mv[n * NG + c] = 0u;
+          for (int c = 0; c < NG; ++c) mk[n][c] = mv[n][c] = 0u;
         }
     }
 
-    // S^T: rows g and g + 8 of product `mt` are tokens 4 g + 2 mt and the next
+    // S^T: rows g and g + 8 of product `mt` are the lane's tokens 2 mt and 2 mt + 1
     float s[NT][2][4];  // [column][token]
 #pragma unroll
     for (int mt = 0; mt < 2; ++mt) {
@@ -312,12 +434,15 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 3 : 2) kv_attention_ker
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
         for (int n = 0; n < NG; ++n) acc[nt][n][0] = acc[nt][n][1] = acc[nt][n][2] = acc[nt][n][3] = 0.0f;
+      uint32_t k0[J], k1[J];
+      load_words<J>(k0, x + (tau_g + 16 * mt) * (D / 2) + t * (D / 8));
+      load_words<J>(k1, x + (tau_g + 16 * mt + 8) * (D / 2) + t * (D / 8));
 #pragma unroll
       for (int j = 0; j < J; ++j) {
-        const uint32_t w0 = cur.k[2 * mt][j], w1 = cur.k[2 * mt + 1][j];
-        const uint32_t a0 = centered<false>(w0), a1 = centered<false>(w1), a2 = centered<true>(w0), a3 = centered<true>(w1);
-        const uint32_t b0 = centered<false>(w0 >> 8), b1 = centered<false>(w1 >> 8), b2 = centered<true>(w0 >> 8),
-                       b3 = centered<true>(w1 >> 8);
+        const uint32_t w0 = k0[j], w1 = k1[j];
+        const uint32_t a0 = centered<false>(w0, exponent), a1 = centered<false>(w1, exponent), a2 = centered<true>(w0, exponent), a3 = centered<true>(w1, exponent);
+        const uint32_t b0 = centered<false>(w0 >> 8, exponent), b1 = centered<false>(w1 >> 8, exponent), b2 = centered<true>(w0 >> 8, exponent),
+                       b3 = centered<true>(w1 >> 8, exponent);
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
           mma16816(acc[nt][j / JG], a0, a1, a2, a3, qf[nt][j][0], qf[nt][j][1]);
@@ -333,9 +458,9 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 3 : 2) kv_attention_ker
             float sum = 0.0f;
 #pragma unroll
             for (int c = 0; c < NG; ++c) {
-              const uint32_t w = cur.mk[(2 * mt + n) * NG + c];
-              const float sc = ops::load16(static_cast<uint16_t>(w), kv.bf16);
-              const float lo = fmaf(sc, 8.0f, ops::load16(static_cast<uint16_t>(w >> 16), kv.bf16));
+              const uint32_t w = mk[2 * mt + n][c];
+              const float sc = pair_scale<BF>(w);
+              const float lo = fmaf(sc, 8.0f, pair_low<BF>(w));
               sum += fmaf(sc, acc[nt][c][2 * n + i], lo * qs[nt][i][c]);
             }
             s[nt][i][2 * mt + n] = sum * cf[nt][i];
@@ -348,15 +473,16 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 3 : 2) kv_attention_ker
         for (int i = 0; i < 2; ++i)
 #pragma unroll
           for (int n = 0; n < 4; ++n)
-            if (!cur.ok || tok0 + n >= lim[nt][i]) s[nt][i][n] = -INFINITY;
+            if (!ok[n >> 1] || tok0 + 8 * n >= lim[nt][i]) s[nt][i][n] = -INFINITY;
     }
     if (a.scores && t < 2) {
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
         for (int i = 0; i < 2; ++i)
-          *reinterpret_cast<float4*>(a.scores + (static_cast<int64_t>(bh) * a.rows_pad + r0 + 4 * nt + 2 * t + i) * a.score_stride +
-                                     tok0) = make_float4(s[nt][i][0], s[nt][i][1], s[nt][i][2], s[nt][i][3]);
+#pragma unroll
+          for (int n = 0; n < 4; ++n)
+            a.scores[(static_cast<int64_t>(bh) * a.rows_pad + r0 + 4 * nt + 2 * t + i) * a.score_stride + tok0 + 8 * n] = s[nt][i][n];
     }
 
     // running maximum; sums are rescaled only when one of the warp's rises
@@ -403,20 +529,37 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 3 : 2) kv_attention_ker
         }
       }
 
+    // V of contraction steps 2 t and 2 t + 1 (mt, half by half): channels 32 j + 4 g + 0..3
+    uint32_t v[4][2][J / 2];
+#pragma unroll
+    for (int n = 0; n < 4; ++n) {
+      load_words<J / 2>(v[n][0], x + L::kV + (tau_v + 8 * n) * (D / 2) + g * (D / 16));
+      load_words<J / 2>(v[n][1], x + L::kV + (tau_w + 8 * n) * (D / 2) + g * (D / 16));
+    }
 #pragma unroll
     for (int c = 0; c < NG; ++c) {
       float sv[4], lo[4];
-      uint32_t top_s = 0;
+      uint32_t top_s = 0;  // bits of the largest scale, which has no sign
 #pragma unroll
       for (int n = 0; n < 4; ++n) {
-        const uint32_t w = cur.mv[n * NG + c];
-        sv[n] = ops::load16(static_cast<uint16_t>(w), kv.bf16);
-        lo[n] = fmaf(sv[n], 8.0f, ops::load16(static_cast<uint16_t>(w >> 16), kv.bf16));
-        const uint32_t bits = __float_as_uint(fabsf(sv[n]));
-        if (bits < 0x7F800000u) top_s = max(top_s, bits);
+        const uint32_t w = mv[n][c];
+        sv[n] = pair_scale<BF>(w);
+        lo[n] = fmaf(sv[n], 8.0f, pair_low<BF>(w));
+        top_s = max(top_s, w & 0xFFFFu);
       }
-      // p s is held as p s 2^(14 - e), e the exponent of the largest s so far
-      const int e_new = static_cast<int>(__reduce_max_sync(kFull, top_s) >> 23);
+      // p s is held as p s 2^(14 - e), e the exponent of the largest finite s so far
+      top_s = __reduce_max_sync(kFull, top_s);
+      constexpr uint32_t kInf = BF ? 0x7F80u : 0x7C00u;
+      if (top_s >= kInf) {
+        top_s = 0;
+#pragma unroll
+        for (int n = 0; n < 4; ++n) {
+          const uint32_t v = mv[n][c] & 0xFFFFu;
+          top_s = max(top_s, v < kInf ? v : 0u);
+        }
+        top_s = __reduce_max_sync(kFull, top_s);
+      }
+      const int e_new = static_cast<int>(__float_as_uint(pair_scale<BF>(top_s)) >> 23);
       if (e_new > e_run[c]) {
         const float f = e_new - e_run[c] > 126 ? 0.0f : pow2(e_run[c] - e_new);
 #pragma unroll
@@ -439,28 +582,26 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 3 : 2) kv_attention_ker
           float x[2];
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
-            const bool hidden = edge && tok0 + n >= lim[nt][i];  // 0 times a NaN that other rows see
+            const bool hidden = edge && tok0 + 8 * n >= lim[nt][i];  // 0 times a NaN that other rows see
             x[i] = hidden ? 0.0f : s[nt][i][n] * (sv[n] * f);
             lsum[nt][i][c] += hidden ? 0.0f : s[nt][i][n] * lo[n];
+            // columns 4..7 take what fp16's 11 bits, cut toward zero, leave
+            x[i] -= __uint_as_float(__float_as_uint(x[i]) & rest_mask);
           }
-          const __half2 hi = __floats2half2_rn(x[0], x[1]);
-          const float2 back = __half22float2(hi);
-          const uint32_t rest = pack_half2(x[0] - back.x, x[1] - back.y);
-          pf[nt][n] = transpose8x8(t < 2 ? *reinterpret_cast<const uint32_t*>(&hi) : rest);
+          pf[nt][n] = transpose8x8(pack_half2_rz(x[0], x[1]));
         }
       }
 #pragma unroll
       for (int j = c * JG; j < (c + 1) * JG; ++j)
 #pragma unroll
         for (int mt = 0; mt < 2; ++mt) {
-          // tokens 8 t + 2 mt and 8 t + 4 + 2 mt, then the ones after each
           constexpr uint32_t kLow = 0x5410u, kHigh = 0x7632u;
           const uint32_t sel = (j & 1) ? kHigh : kLow;
-          const uint32_t p0 = __byte_perm(cur.v[2 * mt][j / 2], cur.v[2 * mt + 4][j / 2], sel);
-          const uint32_t p1 = __byte_perm(cur.v[2 * mt + 1][j / 2], cur.v[2 * mt + 5][j / 2], sel);
-          const uint32_t a0 = centered<false>(p0), a1 = centered<true>(p0), a2 = centered<false>(p1), a3 = centered<true>(p1);
-          const uint32_t b0 = centered<false>(p0 >> 8), b1 = centered<true>(p0 >> 8), b2 = centered<false>(p1 >> 8),
-                         b3 = centered<true>(p1 >> 8);
+          const uint32_t p0 = __byte_perm(v[2 * mt][0][j / 2], v[2 * mt][1][j / 2], sel);
+          const uint32_t p1 = __byte_perm(v[2 * mt + 1][0][j / 2], v[2 * mt + 1][1][j / 2], sel);
+          const uint32_t a0 = centered<false>(p0, exponent), a1 = centered<true>(p0, exponent), a2 = centered<false>(p1, exponent), a3 = centered<true>(p1, exponent);
+          const uint32_t b0 = centered<false>(p0 >> 8, exponent), b1 = centered<true>(p0 >> 8, exponent), b2 = centered<false>(p1 >> 8, exponent),
+                         b3 = centered<true>(p1 >> 8, exponent);
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt) {
             mma16816(o[j][0][nt], a0, a1, a2, a3, pf[nt][2 * mt], pf[nt][2 * mt + 1]);
@@ -468,9 +609,9 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 3 : 2) kv_attention_ker
           }
         }
     }
-    cur = nxt;
-    tile = next;
+    __syncwarp();  // the stage may be filled again
   }
+  __syncthreads();  // every ring is idle: the sums take their place
 
   // the warp's sums to shared memory, in natural units
 #pragma unroll
@@ -501,7 +642,7 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 3 : 2) kv_attention_ker
       }
     }
   __syncthreads();
-  const bool direct = a.splits == 1 && !a.scores;
+  const bool whole = n_rounds == rounds;
   for (int idx = threadIdx.x; idx < ROWS * D; idx += kWarps * 32) {
     const int row = idx / D, d = idx - row * D, r = r0 + row;
     float top = s_m[0][row];
@@ -516,118 +657,156 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 3 : 2) kv_attention_ker
       den += f * s_l[w][row];
     }
     if (r >= a.rows) continue;
-    if (direct) {
+    if (whole) {
       const int tok = r / a.per;
       a.out[(static_cast<int64_t>(b) * a.n_new + tok) * a.out_stride + (h * a.per + r - tok * a.per) * D + d] =
-          ops::store16(den == 0.0f ? 0.0f : sum / den, kv.bf16);
+          ops::store16(den == 0.0f ? 0.0f : sum / den, BF);
+      if (a.scores && d == 0) a.unit_ml[static_cast<int64_t>(bh) * a.rows_pad + r] = make_float2(top, den);
     } else {
-      const int64_t at = (static_cast<int64_t>(bh) * a.rows_pad + r) * a.splits + split;
-      a.part_o[at * D + d] = sum;
-      if (d == 0) a.part_ml[at] = make_float2(top, den);
+      const int64_t slot = (2 * static_cast<int64_t>(blockIdx.x) + (first_segment ? 0 : 1)) * ROWS + row;
+      a.part_o[slot * D + d] = sum;
+      if (d == 0) a.part_ml[slot] = make_float2(top, den);
     }
+  }
+  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // bulk copies will overwrite what was read here
+  __syncthreads();
   }
 }
 
-// Joins the splits: the first batch * heads * rows CTAs each write one output
-// row; the others add the weights exp2(S - lse) of 4 * blockDim tokens of one
-// (sequence, head) to the mass, every element by one thread in one order.
-template <int D>
-__global__ void __launch_bounds__(128) kv_join_kernel(const __grid_constant__ KvAttnArgs a) {
-  __shared__ float s_w[kMaxSplits];
+// The partial sums of unit `unit` of sequence b: those of CTAs first .. last,
+// the first's in slot `slot` and the others' in slot 0. False if one CTA wrote
+// the unit out (or there is none).
+struct Parts {
+  int first, last, slot;
+};
+__device__ __forceinline__ bool parts_of(const KvAttnArgs& a, int b, int unit, int lane, Parts& p) {
+  const int rounds = rounds_of(a, b);
+  if (rounds == 0) return false;
+  const int units_b = a.kv.heads * a.row_blocks;
+  const int64_t total = rounds_before(a, a.batch, lane) * units_b;
+  const int64_t lo = rounds_before(a, b, lane) * units_b + static_cast<int64_t>(unit) * rounds, hi = lo + rounds;
+  const int busy = busy_ctas(total, a.ctas);
+  // CTA c holds round x if run_start(c) <= x < run_start(c + 1): the largest c with total c / busy < x + 1
+  auto holder = [&](int64_t x) { return static_cast<int>(((x + 1) * busy - 1) / total); };
+  p.first = holder(lo);
+  p.last = holder(hi - 1);
+  if (p.first == p.last) return false;
+  // slot 0 if the unit is the first that the CTA works on
+  p.slot = run_start(total, p.first, busy) >= lo ? 0 : 1;
+  return true;
+}
+
+// Joins the partial sums: CTAs before `n_units` each write the output rows of a
+// unit; the others (tracked calls) add the weights exp2(S - lse) of 512 tokens
+// of one (sequence, head) to the mass, every element by one thread in one
+// order.
+template <int D, int ROWS>
+__global__ void __launch_bounds__(512) kv_join_kernel(const __grid_constant__ KvAttnArgs a) {
+  constexpr int GROUPS = 512 / D;  // partial sums read at a time
+  __shared__ float s_sum[GROUPS][D];
   __shared__ float s_lse[STAGQ_KV_MAX_NEW * STAGQ_KV_MAX_SHARE];
   grid_launch_dependents();
   grid_dependency_wait();
   const KvView& kv = a.kv;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int64_t n_rows = static_cast<int64_t>(a.batch) * kv.heads * a.rows;
-  if (blockIdx.x < n_rows) {
-    const int bh = blockIdx.x / a.rows, r = blockIdx.x - bh * a.rows;
-    const int b = bh / kv.heads, h = bh - b * kv.heads;
-    const int64_t at = (static_cast<int64_t>(bh) * a.rows_pad + r) * a.splits;
-    float top = -INFINITY;
-    for (int s = lane; s < a.splits; s += 32) top = fmaxf(top, a.part_ml[at + s].x);
+  const int n_units = a.batch * kv.heads * a.row_blocks;
+  // a row's maximum, and its denominator, over the partial sums of its unit
+  auto row_sum = [&](const Parts& p, int row, float& top, float& den) {
+    top = -INFINITY;
+    for (int c = p.first + lane; c <= p.last; c += 32)
+      top = fmaxf(top, a.part_ml[(2 * static_cast<int64_t>(c) + (c == p.first ? p.slot : 0)) * ROWS + row].x);
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) top = fmaxf(top, __shfl_xor_sync(kFull, top, d));
     const float base = top == -INFINITY ? 0.0f : top;
-    float den = 0.0f;
-    for (int s = lane; s < a.splits; s += 32) {
-      const float2 ml = a.part_ml[at + s];
-      const float f = ex2(ml.x - base);
-      if (warp == 0) s_w[s] = f;
-      den += f * ml.y;
+    den = 0.0f;
+    for (int c = p.first + lane; c <= p.last; c += 32) {
+      const float2 ml = a.part_ml[(2 * static_cast<int64_t>(c) + (c == p.first ? p.slot : 0)) * ROWS + row];
+      den += ex2(ml.x - base) * ml.y;
     }
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) den += __shfl_xor_sync(kFull, den, d);
-    __syncthreads();
-    const int d = threadIdx.x;
-    if (d >= D) return;
+  };
+  Parts p;
+  if (static_cast<int64_t>(blockIdx.x) < static_cast<int64_t>(n_units) * ROWS) {
+    const int u = blockIdx.x / ROWS, row = blockIdx.x - u * ROWS;
+    const int b = u / (kv.heads * a.row_blocks), unit = u - b * kv.heads * a.row_blocks;
+    const int h = unit / a.row_blocks, r = (unit - h * a.row_blocks) * ROWS + row;
+    if (r >= a.rows || !parts_of(a, b, unit, lane, p)) return;
+    float top, den;
+    row_sum(p, row, top, den);
+    const float base = top == -INFINITY ? 0.0f : top;
+    const int group = threadIdx.x / D, d = threadIdx.x - group * D;
     float sum = 0.0f;
-#pragma unroll 8
-    for (int s = 0; s < a.splits; ++s) sum += s_w[s] * a.part_o[(at + s) * D + d];
+#pragma unroll 4
+    for (int c = p.first + group; c <= p.last; c += GROUPS) {
+      const int64_t slot = (2 * static_cast<int64_t>(c) + (c == p.first ? p.slot : 0)) * ROWS + row;
+      sum += ex2(a.part_ml[slot].x - base) * a.part_o[slot * D + d];
+    }
+    s_sum[group][d] = sum;
+    __syncthreads();
+    if (threadIdx.x >= D) return;
+#pragma unroll
+    for (int i = 1; i < GROUPS; ++i) sum += s_sum[i][d];
     const int tok = r / a.per;
     a.out[(static_cast<int64_t>(b) * a.n_new + tok) * a.out_stride + (h * a.per + r - tok * a.per) * D + d] =
         ops::store16(den == 0.0f ? 0.0f : sum / den, kv.bf16);
     return;
   }
   const int chunks = (a.max_len + 511) / 512;
-  const int unit = static_cast<int>(blockIdx.x - n_rows);
-  const int bh = unit / chunks, t0 = (unit - bh * chunks) * 512;
+  const int which = static_cast<int>(blockIdx.x - static_cast<int64_t>(n_units) * ROWS);
+  const int bh = which / chunks, tok = (which - bh * chunks) * 512 + threadIdx.x;
   const int b = bh / kv.heads, h = bh - b * kv.heads;
   const int len = clamped_len(a, b);
-  if (t0 >= len) return;
-  for (int r = warp; r < a.rows; r += 4) {
-    const int64_t at = (static_cast<int64_t>(bh) * a.rows_pad + r) * a.splits;
-    float top = -INFINITY;
-    for (int s = lane; s < a.splits; s += 32) top = fmaxf(top, a.part_ml[at + s].x);
-#pragma unroll
-    for (int d = 1; d < 32; d <<= 1) top = fmaxf(top, __shfl_xor_sync(kFull, top, d));
-    const float base = top == -INFINITY ? 0.0f : top;
-    float den = 0.0f;
-    for (int s = lane; s < a.splits; s += 32) {
-      const float2 ml = a.part_ml[at + s];
-      den += ex2(ml.x - base) * ml.y;
+  if (tok - static_cast<int>(threadIdx.x) >= len) return;
+  for (int rb = 0; rb < a.row_blocks; ++rb) {
+    const bool parts = parts_of(a, b, h * a.row_blocks + rb, lane, p);
+    for (int row = warp; row < ROWS && rb * ROWS + row < a.rows; row += 16) {
+      float top, den;
+      if (parts) {
+        row_sum(p, row, top, den);
+      } else {
+        const float2 ml = a.unit_ml[static_cast<int64_t>(bh) * a.rows_pad + rb * ROWS + row];
+        top = ml.x;
+        den = ml.y;
+      }
+      if (lane == 0) s_lse[rb * ROWS + row] = (top == -INFINITY ? 0.0f : top) + log2f(den);
     }
-#pragma unroll
-    for (int d = 1; d < 32; d <<= 1) den += __shfl_xor_sync(kFull, den, d);
-    if (lane == 0) s_lse[r] = base + log2f(den);
   }
   __syncthreads();
-  float* mass = a.mass + b * a.mass_stride_b + h * a.mass_stride_h;
-  const float* scores = a.scores + static_cast<int64_t>(bh) * a.rows_pad * a.score_stride;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int tok = t0 + 128 * i + threadIdx.x;
-    if (tok >= len) break;
-    float sum = 0.0f;
-    for (int r = 0; r < a.rows; ++r)
-      if (tok < row_limit(a, len, r)) sum += ex2(scores[r * a.score_stride + tok] - s_lse[r]);
-    mass[tok] += sum;
-  }
+  if (tok >= len) return;
+  const float* scores = a.scores + static_cast<int64_t>(bh) * a.rows_pad * a.score_stride + tok;
+  float sum = 0.0f;
+#pragma unroll 4
+  for (int r = 0; r < a.rows; ++r)
+    if (tok < row_limit(a, len, r)) sum += ex2(scores[r * a.score_stride] - s_lse[r]);
+  a.mass[b * a.mass_stride_b + h * a.mass_stride_h + tok] += sum;
 }
 
-template <int D, int NG, int NT>
+template <int D, int NG, int NT, bool BF>
 cudaError_t launch_attention(const KvAttnArgs& a, cudaStream_t s) {
-  const int64_t ctas = static_cast<int64_t>(a.batch) * a.kv.heads * a.row_blocks * a.splits;
-  cudaError_t e = launch_op(kv_attention_kernel<D, NG, NT>, dim3(static_cast<unsigned>(ctas)), dim3(kWarps * 32), 0, s, a);
-  if (e != cudaSuccess || (a.splits == 1 && !a.scores)) return e;
-  int64_t join = static_cast<int64_t>(a.batch) * a.kv.heads * a.rows;
+  constexpr int smem = kWarps * kStages * TileLayout<D, NG>::kBytes;
+  cudaError_t e = cudaFuncSetAttribute(kv_attention_kernel<D, NG, NT, BF>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) return e;
+  e = launch_op(kv_attention_kernel<D, NG, NT, BF>, dim3(a.ctas), dim3(kWarps * 32), smem, s, a);
+  if (e != cudaSuccess || !a.part_o) return e;
+  int64_t join = static_cast<int64_t>(a.batch) * a.kv.heads * a.row_blocks * 4 * NT;
   if (a.scores) join += static_cast<int64_t>(a.batch) * a.kv.heads * ((a.max_len + 511) / 512);
-  return launch_op(kv_join_kernel<D>, dim3(static_cast<unsigned>(join)), dim3(128), 0, s, a);
+  return launch_op(kv_join_kernel<D, 4 * NT>, dim3(static_cast<unsigned>(join)), dim3(512), 0, s, a);
 }
 
 template <int D, int NG>
 cudaError_t launch_nt(const KvAttnArgs& a, int nt, cudaStream_t s) {
-  return nt == 1 ? launch_attention<D, NG, 1>(a, s) : launch_attention<D, NG, 2>(a, s);
+  if (a.kv.bf16) return nt == 1 ? launch_attention<D, NG, 1, true>(a, s) : launch_attention<D, NG, 2, true>(a, s);
+  return nt == 1 ? launch_attention<D, NG, 1, false>(a, s) : launch_attention<D, NG, 2, false>(a, s);
 }
 
 int64_t align256(int64_t v) { return (v + 255) / 256 * 256; }
 
 }  // namespace
 
-// Four query rows of a KV head per CTA, eight where there are more than four
-// (the cache is then read once per eight rows). The tokens are split until the
-// CTAs fill the GPU three times over (three fit an SM), but a split keeps
-// one tile for each warp.
+// Four query rows of a KV head per unit, eight where there are more than four
+// (the cache is then read once per eight rows). As many CTAs as fit the GPU at
+// once, but no more than there can be rounds. Units of one round need no join.
 KvAttnPlan plan_kv_attention(int batch, int heads, int q_heads, int n_new, int dim, int max_len, bool mass,
                              int num_sms) {
   KvAttnPlan p{};
@@ -636,21 +815,21 @@ KvAttnPlan plan_kv_attention(int batch, int heads, int q_heads, int n_new, int d
   p.row_blocks = (rows + 4 * p.nt - 1) / (4 * p.nt);
   p.rows_pad = p.row_blocks * 4 * p.nt;
   const int64_t units = static_cast<int64_t>(batch) * heads * p.row_blocks;
-  const int64_t tiles = (static_cast<int64_t>(max_len) + kTile - 1) / kTile;
-  int64_t splits = (static_cast<int64_t>(num_sms) * (p.nt == 1 ? 3 : 2)) / units;
-  const int64_t most = (tiles + kWarps - 1) / kWarps;
-  if (splits > most) splits = most;
-  if (splits > kMaxSplits) splits = kMaxSplits;
-  if (splits < 1) splits = 1;
-  p.splits = static_cast<int>(splits);
-  p.score_stride = mass ? tiles * kTile : 0;
-  if (p.splits > 1 || mass) {
-    const int64_t parts = static_cast<int64_t>(batch) * heads * p.rows_pad * p.splits;
-    p.off_ml = 0;
-    p.off_o = align256(parts * 8);
-    p.off_scores = p.off_o + align256(parts * dim * 4);
-    p.bytes = p.off_scores + align256(static_cast<int64_t>(batch) * heads * p.rows_pad * p.score_stride * 4);
+  const int64_t rounds = (static_cast<int64_t>(max_len) + kWarps * kTile - 1) / (kWarps * kTile);
+  const int64_t fit = static_cast<int64_t>(num_sms) * (p.nt == 1 ? 4 : 2);
+  p.score_stride = mass ? rounds * kWarps * kTile : 0;
+  if (rounds == 1 && !mass) {
+    p.ctas = static_cast<int>(units);
+    return p;
   }
+  p.ctas = static_cast<int>(units * rounds < fit ? units * rounds : fit);
+  const int64_t slots = 2 * static_cast<int64_t>(p.ctas) * 4 * p.nt;
+  p.off_ml = 0;
+  p.off_o = align256(slots * 8);
+  p.off_unit = p.off_o + align256(slots * dim * 4);
+  const int64_t rows_all = static_cast<int64_t>(batch) * heads * p.rows_pad;
+  p.off_scores = p.off_unit + (mass ? align256(rows_all * 8) : 0);
+  p.bytes = p.off_scores + align256(rows_all * p.score_stride * 4);
   return p;
 }
 

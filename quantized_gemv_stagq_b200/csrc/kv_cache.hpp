@@ -40,11 +40,12 @@ struct KvAttnArgs {
   const int32_t* lens;
   float* mass;             // null: not tracked
   int64_t mass_stride_b, mass_stride_h;
-  float* part_o;           // [batch * heads * rows_pad][splits][dim]
-  float2* part_ml;         // [batch * heads * rows_pad][splits]
+  float* part_o;           // partial sums: [ctas][2][rows of a block][dim]; null: no unit is shared
+  float2* part_ml;         // their maxima and denominators
+  float2* unit_ml;         // tracked: the same of the rows that one CTA finished, [batch * heads][rows_pad]
   float* scores;           // [batch * heads][rows_pad][score_stride]
   int64_t score_stride;
-  int32_t batch, q_heads, per, n_new, rows, rows_pad, row_blocks, splits, max_len, vec;
+  int32_t batch, q_heads, per, n_new, rows, rows_pad, row_blocks, ctas, max_len, vec;
   float scale_log2;        // softmax scale times log2(e)
 };
 
@@ -61,9 +62,9 @@ struct KvEvictArgs {
 
 struct KvAttnPlan {
   int nt;                  // query rows per CTA: 4 * nt
-  int row_blocks, splits, rows_pad;
+  int row_blocks, ctas, rows_pad;
   int64_t score_stride;
-  int64_t off_ml, off_o, off_scores, bytes;  // workspace layout
+  int64_t off_ml, off_o, off_unit, off_scores, bytes;  // workspace layout
 };
 
 KvAttnPlan plan_kv_attention(int batch, int heads, int q_heads, int n_new, int dim, int max_len, bool mass,

@@ -224,9 +224,11 @@ const char* attention_error(const stagq_kv_cache* c, int32_t batch, int32_t max_
   if (q_heads < 1 || q_heads % c->heads) return "q_heads must be a multiple of the cache's heads";
   if (q_heads / c->heads > STAGQ_KV_MAX_SHARE) return "more than STAGQ_KV_MAX_SHARE query heads per KV head";
   if (n_new < 1 || n_new > STAGQ_KV_MAX_NEW) return "n_new outside 1..STAGQ_KV_MAX_NEW";
-  // the join's grid: rows, and 512 tokens of a head per CTA
+  // the join's grid: rows in blocks of up to 8, and 512 tokens of a head per CTA
   const int64_t heads = static_cast<int64_t>(batch) * c->heads;
-  if (heads * (q_heads / c->heads * n_new + (max_len + 511) / 512 + 512) > INT_MAX) return "too many rows for one call";
+  if (heads * (q_heads / c->heads * n_new + 8 + (static_cast<int64_t>(max_len) + 511) / 512) > INT_MAX) return "too many rows for one call";
+  // rounds times CTAs, and scores, in 64 bits
+  if (heads * (q_heads / c->heads * n_new + 8) > (static_cast<int64_t>(1) << 58) / (static_cast<int64_t>(max_len) + 128) / 4) return "too many rows for one call";
   return nullptr;
 }
 
@@ -281,7 +283,10 @@ extern "C" int stagq_kv_attention(const stagq_kv_cache* c, const stagq_kv_table*
   if (p.bytes) {
     a.part_ml = reinterpret_cast<float2*>(ws + p.off_ml);
     a.part_o = reinterpret_cast<float*>(ws + p.off_o);
-    if (mass) a.scores = reinterpret_cast<float*>(ws + p.off_scores);
+    if (mass) {
+      a.unit_ml = reinterpret_cast<float2*>(ws + p.off_unit);
+      a.scores = reinterpret_cast<float*>(ws + p.off_scores);
+    }
   }
   a.score_stride = p.score_stride;
   a.batch = t->batch;
@@ -291,7 +296,7 @@ extern "C" int stagq_kv_attention(const stagq_kv_cache* c, const stagq_kv_table*
   a.rows = a.per * n_new;
   a.rows_pad = p.rows_pad;
   a.row_blocks = p.row_blocks;
-  a.splits = p.splits;
+  a.ctas = p.ctas;
   a.max_len = max_len;
   a.vec = wide(q, q_stride, 2);
   a.scale_log2 = scale * 1.4426950408889634f;
