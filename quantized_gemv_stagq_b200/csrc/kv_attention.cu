@@ -10,12 +10,15 @@
 // Bound by the cache's bytes as long as the unpacking keeps up: at 6.5 TB/s an
 // SM takes in about 49 codes per clock. What keeps the instruction count near
 // one per two codes:
-//  - Two codes are masked out of a word in place and OR'ed under the exponent
+//  - V: two codes are masked out of a word in place and OR'ed under the exponent
 //    of 1024 in one operation; a packed subtraction leaves u - 8 (16 times that
 //    for the upper 4 bits of a byte) as exact fp16, and lo + 8 s replaces lo.
-//    Without the subtraction the masked bits are fp16 subnormals, exact too, and
-//    mma takes them: but it aligns products by their nominal exponents, and the
-//    result was 2e-4 off at 67000 tokens (fp16 rounds by 2e-4), now 2e-7.
+//    The sums over the tokens then stay small: with u itself, whose mean is
+//    7.5, the result was 4e-4 off at 67000 tokens (fp16 rounds by 2e-4).
+//  - K: the same bits without the OR are fp16 subnormals, 16 u 2^-24, exact
+//    too, and mma takes them at full rate; nothing needs to be subtracted. It
+//    aligns products by their nominal exponents, which drops what lies below
+//    2^-18 of the row's largest q: of a score, about 1e-6.
 //  - The order of a contraction is free, so the packed order of a row is the
 //    order of the mma fragments (kv_cache.cu): a lane's K words feed its
 //    A fragments without a shuffle, and two tokens' V words give the pairs of
@@ -37,12 +40,18 @@
 // the end; nothing in the loop waits for another warp.
 //
 // The work is cut into rounds of 128 tokens (a tile per warp) of a unit
-// (sequence, KV head, block of query rows), numbered unit after unit, and every
-// CTA takes an equal run of that numbering, read off the lengths on the
-// device. A ragged batch, one long sequence and many short ones thus fill the
-// GPU alike. A unit that one CTA covers is written out; the others leave a
-// partial sum (at most two per CTA), and a second kernel joins those.
+// (sequence, KV head, block of query rows). Two ways to share it, chosen from
+// the sizes (plan_kv_attention):
+//  - A cluster of up to 8 CTAs per unit, an equal part of its rounds each, that
+//    joins its sums through distributed shared memory: one launch, for calls
+//    of little work.
+//  - As many CTAs as fit the GPU. The rounds are numbered unit after unit and
+//    every CTA takes an equal run of the numbering, read off the lengths on the
+//    device, so that a ragged batch, one long sequence and many short ones fill
+//    the GPU alike. A unit that one CTA covers is written out; the others leave
+//    a partial sum (at most two per CTA), and a second kernel joins those.
 #include <climits>
+#include <cmath>
 
 #include "kernel_common.cuh"
 #include "kv_cache.hpp"
@@ -59,6 +68,7 @@ using kernels::kFull;
 
 constexpr int kWarps = 4;
 constexpr int kTile = 32;            // tokens of a warp's tile
+constexpr int kMaxCluster = 8;
 
 __device__ __forceinline__ float ex2(float x) {
   float y;
@@ -87,10 +97,6 @@ __device__ __forceinline__ uint32_t centered(uint32_t w, uint32_t exponent) {
   asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(v) : "r"(w), "n"(HIGH ? 0x00F000F0 : 0x000F000F), "r"(exponent));
   asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(v), "r"(HIGH ? 0x64806480u : 0x64086408u));
   return r;
-}
-__device__ __forceinline__ uint32_t pack_half2(float lo, float hi) {
-  const __half2 h = __floats2half2_rn(lo, hi);
-  return *reinterpret_cast<const uint32_t*>(&h);
 }
 // Both values toward zero, hi in the upper half.
 __device__ __forceinline__ uint32_t pack_half2_rz(float lo, float hi) {
@@ -128,6 +134,10 @@ __device__ __forceinline__ void load_words(uint32_t (&w)[WORDS], const uint8_t* 
   }
 }
 
+// CTAs that fit an SM by their registers: 128 a thread hold 4 query rows and
+// one group per head without spilling, more groups need 168, 8 rows 255.
+constexpr int resident_ctas(int nt, int groups) { return nt > 1 ? 2 : groups > 1 ? 3 : 4; }
+
 constexpr int kStages = 3;
 constexpr uint64_t kWaitLimitNs = 2000000000ull;
 
@@ -159,32 +169,57 @@ __device__ __forceinline__ int clamped_len(const KvAttnArgs& a, int b) {
 __device__ __forceinline__ int rounds_of(const KvAttnArgs& a, int b) {
   return (clamped_len(a, b) + kWarps * kTile - 1) / (kWarps * kTile);
 }
-// The rounds of the sequences before b, and of all of them. The lanes of a
-// warp take 32 sequences at a time.
-__device__ __forceinline__ int64_t rounds_before(const KvAttnArgs& a, int b, int lane) {
-  int64_t n = 0;
-  for (int i = lane; i < b; i += 32) n += rounds_of(a, i);
-#pragma unroll
-  for (int d = 1; d < 32; d <<= 1) n += __shfl_xor_sync(kFull, n, d);
-  return n;
+// How `total` rounds (positive) are dealt to the CTAs: runs of `base` rounds,
+// the first `rem` CTAs one more; CTAs from `busy` on get none.
+struct Runs {
+  int base, rem, busy;
+  __device__ Runs(int total, int ctas) {
+    busy = min(total, ctas);
+    base = total / busy;
+    rem = total - base * busy;
+  }
+  __device__ int start(int c) const { return c * base + min(c, rem); }
+  // the CTA whose run holds round x
+  __device__ int holder(int x) const {
+    const int longer = rem * (base + 1);
+    return x < longer ? x / (base + 1) : rem + (x - longer) / base;
+  }
+};
+
+__device__ __forceinline__ void cluster_sync_all() {
+  asm volatile("barrier.cluster.arrive;\n\tbarrier.cluster.wait;" ::: "memory");
 }
-// CTAs that get a run of `total` rounds, of at least one round each, and the
-// first round of CTA c's.
-__device__ __forceinline__ int busy_ctas(int64_t total, int ctas) { return total < ctas ? static_cast<int>(total) : ctas; }
-__device__ __forceinline__ int64_t run_start(int64_t total, int c, int busy) { return total * c / busy; }
+__device__ __forceinline__ float load_peer(uint32_t addr, uint32_t rank) {
+  uint32_t peer;
+  float v;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(peer) : "r"(addr), "r"(rank));
+  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(peer) : "memory");
+  return v;
+}
+
+__device__ __forceinline__ float4 load_peer4(uint32_t addr, uint32_t rank) {
+  uint32_t peer;
+  float4 v;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(peer) : "r"(addr), "r"(rank));
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(peer) : "memory");
+  return v;
+}
 
 template <int D, int NG, int NT, bool BF>
-__global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 4 : 2) kv_attention_kernel(const __grid_constant__ KvAttnArgs a) {
+__global__ void __launch_bounds__(kWarps * 32, resident_ctas(NT, NG)) kv_attention_kernel(const __grid_constant__ KvAttnArgs a) {
   constexpr int J = D / 32;       // blocks of 32 channels
   constexpr int JG = J / NG;      // blocks of a group
   constexpr int ROWS = 4 * NT;
   using L = TileLayout<D, NG>;
-  static_assert(kStages * L::kBytes >= ROWS * D * 4, "the warps' sums take the rings' place");
+  static_assert(kStages * L::kBytes >= 2 * ROWS * D * 4, "the warps' sums take the rings' place");
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ float s_m[kWarps][ROWS], s_l[kWarps][ROWS];
   __shared__ __align__(8) uint64_t s_full[kWarps][kStages];
   __shared__ uint32_t s_ok[kWarps][kStages];  // by lane: whether its piece's page is in the pool
-  float (*s_o)[ROWS][D] = reinterpret_cast<float (*)[ROWS][D]>(smem);
+  __shared__ float s_top[ROWS], s_den[ROWS];  // of the CTA, for its cluster
+  __shared__ __align__(16) uint16_t s_q[ROWS][D];
+  __shared__ float s_cf[ROWS], s_qs[ROWS][NG];
+  float (*s_o)[2 * ROWS][D] = reinterpret_cast<float (*)[2 * ROWS][D]>(smem);  // 8 columns for 4 rows
 
   grid_launch_dependents();
   grid_dependency_wait();
@@ -209,52 +244,71 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 4 : 2) kv_attention_ker
   const int copy_src = (kind & 1) * kv.block_bytes + (kind < 2 ? 0 : kv.page * (D / 2));
   const int copy_bytes = piece_tokens * row_bytes;
 
-  for (int i = blockIdx.x; i < a.batch; i += gridDim.x) {  // sequences without a token have no unit
-    const int n = a.lens[i];
-    if (threadIdx.x == 0 && (n < 0 || n > a.max_len)) atomicOr(&g_status, kOpsBadPage);
-    if (n <= 0)
-      for (int c = threadIdx.x; c < a.n_new * a.q_heads * D; c += kWarps * 32) {
-        const int tok = c / (a.q_heads * D);
-        a.out[(static_cast<int64_t>(i) * a.n_new + tok) * a.out_stride + c - tok * a.q_heads * D] = 0;
-      }
-  }
-
-  // this CTA's run of rounds, and the sequence b that it starts in
-  const int64_t total = rounds_before(a, a.batch, lane) * units_b;
-  const int busy = busy_ctas(total, gridDim.x);
-  if (static_cast<int>(blockIdx.x) >= busy) return;
-  int64_t at = run_start(total, blockIdx.x, busy);
-  const int64_t run_end = run_start(total, blockIdx.x + 1, busy);
-  int b = 0;
-  int64_t before = 0;  // rounds before sequence b
-  for (int b0 = 0;; b0 += 32) {
-    const int64_t n = b0 + lane < a.batch ? static_cast<int64_t>(rounds_of(a, b0 + lane)) * units_b : 0;
-    int64_t sum = n;  // of this lane's sequence and those before it
+  int at = 0, run_end = 1;  // this CTA's run of rounds; with clusters: one pass
+  int b = 0, before = 0;    // the sequence of round `at`, and the rounds before it
+  Runs runs(1, 1);
+  if (a.cluster == 0) {
+    for (int i = blockIdx.x; i < a.batch; i += gridDim.x) {  // sequences without a token have no unit
+      const int n = a.lens[i];
+      if (threadIdx.x == 0 && (n < 0 || n > a.max_len)) atomicOr(&g_status, kOpsBadPage);
+      if (n <= 0)
+        for (int c = threadIdx.x; c < a.n_new * a.q_heads * D; c += kWarps * 32) {
+          const int tok = c / (a.q_heads * D);
+          a.out[(static_cast<int64_t>(i) * a.n_new + tok) * a.out_stride + c - tok * a.q_heads * D] = 0;
+        }
+    }
+    int total = 0;
+    for (int i = lane; i < a.batch; i += 32) total += rounds_of(a, i) * units_b;
+    total = __reduce_add_sync(kFull, total);
+    if (total == 0) return;
+    runs = Runs(total, gridDim.x);
+    if (static_cast<int>(blockIdx.x) >= runs.busy) return;
+    at = runs.start(blockIdx.x);
+    run_end = runs.start(blockIdx.x + 1);
+    for (int b0 = 0;; b0 += 32) {
+      const int n = b0 + lane < a.batch ? rounds_of(a, b0 + lane) * units_b : 0;
+      int sum = n;  // of this lane's sequence and those before it
 #pragma unroll
-    for (int d = 1; d < 32; d <<= 1) {
-      const int64_t o = __shfl_up_sync(kFull, sum, d);
-      if (lane >= d) sum += o;
+      for (int d = 1; d < 32; d <<= 1) {
+        const int o = __shfl_up_sync(kFull, sum, d);
+        if (lane >= d) sum += o;
+      }
+      const uint32_t past = __ballot_sync(kFull, before + sum > at);
+      if (past) {
+        const int l = __ffs(past) - 1;
+        b = b0 + l;
+        before += __shfl_sync(kFull, sum - n, l);
+        break;
+      }
+      before += __shfl_sync(kFull, sum, 31);
     }
-    const uint32_t past = __ballot_sync(kFull, before + sum > at);
-    if (past) {
-      const int l = __ffs(past) - 1;
-      b = b0 + l;
-      before += __shfl_sync(kFull, sum - n, l);
-      break;
-    }
-    before += __shfl_sync(kFull, sum, 31);
   }
   bool first_segment = true;
   for (; at < run_end; first_segment = false) {
-  int rounds = rounds_of(a, b);
-  while (at >= before + static_cast<int64_t>(rounds) * units_b) {
-    before += static_cast<int64_t>(rounds) * units_b;
-    rounds = rounds_of(a, ++b);
+  int rounds, unit, round0, n_rounds, part = 0;
+  if (a.cluster == 0) {
+    rounds = rounds_of(a, b);
+    while (at >= before + rounds * units_b) {
+      before += rounds * units_b;
+      rounds = rounds_of(a, ++b);
+    }
+    unit = (at - before) / rounds;  // of the sequence
+    round0 = at - before - unit * rounds;
+    n_rounds = min(rounds - round0, run_end - at);
+    if (round0 == 0 && threadIdx.x == 0 && a.part_o)  // where the join finds the unit's partial sums
+      a.parts[b * units_b + unit] = make_int4(blockIdx.x, runs.holder(at + rounds - 1), first_segment ? 0 : 1, 0);
+    at += n_rounds;
+  } else {
+    unit = blockIdx.x / a.cluster;
+    part = blockIdx.x - unit * a.cluster;
+    b = unit / units_b;
+    unit -= b * units_b;
+    if (threadIdx.x == 0 && (a.lens[b] < 0 || a.lens[b] > a.max_len)) atomicOr(&g_status, kOpsBadPage);
+    rounds = rounds_of(a, b);
+    round0 = rounds * part / a.cluster;
+    n_rounds = rounds * (part + 1) / a.cluster - round0;
+    at = run_end;
   }
-  const int unit = static_cast<int>((at - before) / rounds);  // of the sequence
-  const int round0 = static_cast<int>((at - before) - static_cast<int64_t>(unit) * rounds);
-  const int n_rounds = static_cast<int>(min(static_cast<int64_t>(rounds - round0), run_end - at));
-  at += n_rounds;
   const int h = unit / a.row_blocks, rb = unit - h * a.row_blocks;
   const int bh = b * kv.heads + h;
   const int r0 = rb * ROWS;
@@ -293,69 +347,58 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 4 : 2) kv_attention_ker
     }
 
   // q in fp16, each row scaled by a power of two so that its largest value is
-  // in [2^10, 2^11): exact for fp16 and bf16 alike (and q / 16 too), down to
-  // values 2^-34 of the row's largest.
-  uint32_t qf[NT][J][4];
-  float cf[NT][2], qs[NT][2][NG];
-  int lim[NT][2];
+  // in [2^10, 2^11): exact for fp16 and bf16 alike, down to values 2^-24 of the
+  // row's largest. A warp takes a row, a lane one channel of each 32; each
+  // eight channels lie in the order of the fragments: 0, 4, 1, 5, 2, 6, 3, 7.
 #pragma unroll
-  for (int nt = 0; nt < NT; ++nt) {
-    const int r = r0 + 4 * nt + (g & 3);
-    float x[J][8];
-    float amax = 0.0f;
-    bool fine = true;
+  for (int row = warp; row < ROWS; row += kWarps) {
+    const int r = r0 + row, tok = r / a.per;
+    const uint16_t* q = a.q + (static_cast<int64_t>(b) * a.n_new + tok) * a.q_stride + (h * a.per + r - tok * a.per) * D;
+    float x[J], sum[NG];
+    uint32_t top = 0;  // bits of the largest magnitude
 #pragma unroll
     for (int j = 0; j < J; ++j) {
-      uint16_t raw[8] = {};
-      if (r < a.rows) {
-        const int tok = r / a.per;
-        ops::load8(a.q + (static_cast<int64_t>(b) * a.n_new + tok) * a.q_stride + (h * a.per + r - tok * a.per) * D + 32 * j + 8 * t,
-                   a.vec, raw);
-      }
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        x[j][i] = ops::load16(raw[i], BF);
-        fine = fine && isfinite(x[j][i]);
-        amax = fmaxf(amax, fabsf(x[j][i]));
-      }
+      x[j] = r < a.rows ? ops::load16(q[32 * j + lane], BF) : 0.0f;
+      top = max(top, __float_as_uint(x[j]) & 0x7FFFFFFFu);
     }
-#pragma unroll
-    for (int d = 1; d < 4; d <<= 1) {
-      amax = fmaxf(amax, __shfl_xor_sync(kFull, amax, d));
-      fine = __shfl_xor_sync(kFull, fine ? 1 : 0, d) && fine;
-    }
-    const int e = fine && amax > 0.0f ? max(-126, static_cast<int>(__float_as_uint(amax) >> 23) - 127 - 10) : 0;
-    const float down = pow2(-e);
-    const float c = fine ? a.scale_log2 * pow2(e) : __uint_as_float(0x7FC00000u);
-    float sum[NG];
+    top = __reduce_max_sync(kFull, top);
+    const bool fine = top < 0x7F800000u;
+    const int e = fine && top ? max(-126, static_cast<int>(top >> 23) - 127 - 10) : 0;
+    const float down = fine ? pow2(-e) : 0.0f;
 #pragma unroll
     for (int n = 0; n < NG; ++n) sum[n] = 0.0f;
 #pragma unroll
     for (int j = 0; j < J; ++j) {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        x[j][i] = fine ? x[j][i] * down : 0.0f;
-        sum[j / JG] += x[j][i];
-      }
-      // word nibbles 0, 4 | 1, 5 (16 times) | 2, 6 | 3, 7 (16 times)
-      qf[nt][j][0] = pack_half2(x[j][0], x[j][4]);
-      qf[nt][j][1] = pack_half2(x[j][1] * 0.0625f, x[j][5] * 0.0625f);
-      qf[nt][j][2] = pack_half2(x[j][2], x[j][6]);
-      qf[nt][j][3] = pack_half2(x[j][3] * 0.0625f, x[j][7] * 0.0625f);
+      x[j] = fine ? x[j] * down : 0.0f;
+      sum[j / JG] += x[j];
+      s_q[row][32 * j + (lane & ~7) + 2 * (lane & 3) + ((lane >> 2) & 1)] = __half_as_ushort(__float2half_rn(x[j]));
     }
 #pragma unroll
-    for (int n = 0; n < NG; ++n) {
-      sum[n] += __shfl_xor_sync(kFull, sum[n], 1);
-      sum[n] += __shfl_xor_sync(kFull, sum[n], 2);
+    for (int n = 0; n < NG; ++n)
+#pragma unroll
+      for (int d = 1; d < 32; d <<= 1) sum[n] += __shfl_xor_sync(kFull, sum[n], d);
+    if (lane == 0) {
+      const float c = fine ? a.scale_log2 * pow2(e) : __uint_as_float(0x7FC00000u);
+      s_cf[row] = c;
+#pragma unroll
+      for (int n = 0; n < NG; ++n) s_qs[row][n] = sum[n] * c;
     }
+  }
+  __syncthreads();
+  uint32_t qf[NT][J][4];
+  float cf[NT][2], qs[NT][2][NG];  // softmax scale of a column, and that times its sums of q
+  int lim[NT][2];
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+    for (int j = 0; j < J; ++j) load_words<4>(qf[nt][j], reinterpret_cast<const uint8_t*>(&s_q[4 * nt + (g & 3)][32 * j + 8 * t]));
 #pragma unroll
     for (int i = 0; i < 2; ++i) {  // this lane's columns 2 t + i are rows (2 t + i) mod 4 of the tile
-      const int row = (2 * t + i) & 3;
-      cf[nt][i] = __shfl_sync(kFull, c, 4 * row);
+      const int row = 4 * nt + ((2 * t + i) & 3);
+      cf[nt][i] = s_cf[row] * 1048576.0f;  // codes count as 2^-20
 #pragma unroll
-      for (int n = 0; n < NG; ++n) qs[nt][i][n] = __shfl_sync(kFull, sum[n], 4 * row);
-      const int rr = r0 + 4 * nt + row;
-      lim[nt][i] = rr < a.rows ? row_limit(a, len, rr) : limmax;
+      for (int n = 0; n < NG; ++n) qs[nt][i][n] = s_qs[row][n];
+      lim[nt][i] = r0 + row < a.rows ? row_limit(a, len, r0 + row) : limmax;
     }
   }
   int lim_min = lim[0][0];
@@ -426,85 +469,78 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 4 : 2) kv_attention_ker
     }
 
     // S^T: rows g and g + 8 of product `mt` are the lane's tokens 2 mt and 2 mt + 1
-    float s[NT][2][4];  // [column][token]
+    float acc[2][NT][NG][4];
 #pragma unroll
     for (int mt = 0; mt < 2; ++mt) {
-      float acc[NT][NG][4];
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-        for (int n = 0; n < NG; ++n) acc[nt][n][0] = acc[nt][n][1] = acc[nt][n][2] = acc[nt][n][3] = 0.0f;
+        for (int n = 0; n < NG; ++n) acc[mt][nt][n][0] = acc[mt][nt][n][1] = acc[mt][nt][n][2] = acc[mt][nt][n][3] = 0.0f;
       uint32_t k0[J], k1[J];
       load_words<J>(k0, x + (tau_g + 16 * mt) * (D / 2) + t * (D / 8));
       load_words<J>(k1, x + (tau_g + 16 * mt + 8) * (D / 2) + t * (D / 8));
 #pragma unroll
       for (int j = 0; j < J; ++j) {
-        const uint32_t w0 = k0[j], w1 = k1[j];
-        const uint32_t a0 = centered<false>(w0, exponent), a1 = centered<false>(w1, exponent), a2 = centered<true>(w0, exponent), a3 = centered<true>(w1, exponent);
-        const uint32_t b0 = centered<false>(w0 >> 8, exponent), b1 = centered<false>(w1 >> 8, exponent), b2 = centered<true>(w0 >> 8, exponent),
-                       b3 = centered<true>(w1 >> 8, exponent);
+        constexpr uint32_t M = 0x00F000F0u;
+        const uint32_t a0 = (k0[j] << 4) & M, a1 = (k1[j] << 4) & M, a2 = k0[j] & M, a3 = k1[j] & M;
+        const uint32_t b0 = (k0[j] >> 4) & M, b1 = (k1[j] >> 4) & M, b2 = (k0[j] >> 8) & M, b3 = (k1[j] >> 8) & M;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
-          mma16816(acc[nt][j / JG], a0, a1, a2, a3, qf[nt][j][0], qf[nt][j][1]);
-          mma16816(acc[nt][j / JG], b0, b1, b2, b3, qf[nt][j][2], qf[nt][j][3]);
+          mma16816(acc[mt][nt][j / JG], a0, a1, a2, a3, qf[nt][j][0], qf[nt][j][1]);
+          mma16816(acc[mt][nt][j / JG], b0, b1, b2, b3, qf[nt][j][2], qf[nt][j][3]);
         }
       }
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-        for (int n = 0; n < 2; ++n)
-#pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            float sum = 0.0f;
-#pragma unroll
-            for (int c = 0; c < NG; ++c) {
-              const uint32_t w = mk[2 * mt + n][c];
-              const float sc = pair_scale<BF>(w);
-              const float lo = fmaf(sc, 8.0f, pair_low<BF>(w));
-              sum += fmaf(sc, acc[nt][c][2 * n + i], lo * qs[nt][i][c]);
-            }
-            s[nt][i][2 * mt + n] = sum * cf[nt][i];
-          }
     }
-    if (edge) {
+    // scores less the reference m of their row, in powers of two
+    float s[NT][2][4];  // [column][token]
+    auto score = [&](const float (&ref)[NT][2]) {
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
+      for (int n = 0; n < 4; ++n)
 #pragma unroll
-        for (int i = 0; i < 2; ++i)
+        for (int c = 0; c < NG; ++c) {
+          const float sc = pair_scale<BF>(mk[n][c]), lo = pair_low<BF>(mk[n][c]);
 #pragma unroll
-          for (int n = 0; n < 4; ++n)
-            if (!ok[n >> 1] || tok0 + 8 * n >= lim[nt][i]) s[nt][i][n] = -INFINITY;
-    }
-    if (a.scores && t < 2) {
+          for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
+            for (int i = 0; i < 2; ++i)
+              s[nt][i][n] = fmaf(acc[n >> 1][nt][c][2 * (n & 1) + i], sc * cf[nt][i],
+                                 fmaf(lo, qs[nt][i][c], c == 0 ? -ref[nt][i] : s[nt][i][n]));
+        }
+      if (edge) {
 #pragma unroll
-        for (int i = 0; i < 2; ++i)
+        for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-          for (int n = 0; n < 4; ++n)
-            a.scores[(static_cast<int64_t>(bh) * a.rows_pad + r0 + 4 * nt + 2 * t + i) * a.score_stride + tok0 + 8 * n] = s[nt][i][n];
-    }
-
-    // running maximum; sums are rescaled only when one of the warp's rises
-    float top[NT][2];
+          for (int i = 0; i < 2; ++i)
+#pragma unroll
+            for (int n = 0; n < 4; ++n)
+              if (!ok[n >> 1] || tok0 + 8 * n >= lim[nt][i]) s[nt][i][n] = -INFINITY;
+      }
+    };
+    score(m);
+    // The reference is no maximum: it follows only when a score exceeds it by
+    // 2^8 (from -inf, the start, any score does), so p is below 2^8 and most
+    // tiles need no reduction over the warp and no rescaling.
     bool rises = false;
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        float x = fmaxf(fmaxf(s[nt][i][0], s[nt][i][1]), fmaxf(s[nt][i][2], s[nt][i][3]));
-#pragma unroll
-        for (int d = 4; d < 32; d <<= 1) x = fmaxf(x, __shfl_xor_sync(kFull, x, d));
-        top[nt][i] = fmaxf(m[nt][i], x);
-        rises = rises || top[nt][i] > m[nt][i];
-      }
+      for (int i = 0; i < 2; ++i)
+        rises = rises || fmaxf(fmaxf(s[nt][i][0], s[nt][i][1]), fmaxf(s[nt][i][2], s[nt][i][3])) > 8.0f;
     if (__any_sync(kFull, rises)) {
+      float zero[NT][2];
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) zero[nt][0] = zero[nt][1] = 0.0f;
+      score(zero);
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-          const float f = top[nt][i] > m[nt][i] ? ex2(m[nt][i] - top[nt][i]) : 1.0f;  // the first time: 0
-          m[nt][i] = top[nt][i];
+          float x = fmaxf(fmaxf(s[nt][i][0], s[nt][i][1]), fmaxf(s[nt][i][2], s[nt][i][3]));
+#pragma unroll
+          for (int d = 4; d < 32; d <<= 1) x = fmaxf(x, __shfl_xor_sync(kFull, x, d));
+          const float top = fmaxf(m[nt][i], x);
+          const float f = top > m[nt][i] ? ex2(m[nt][i] - top) : 1.0f;  // the first time: 0
+          m[nt][i] = top;
           l[nt][i] *= f;
 #pragma unroll
           for (int n = 0; n < NG; ++n) lsum[nt][i][n] *= f;
@@ -516,18 +552,33 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 4 : 2) kv_attention_ker
             o[j][1][nt][2 + i] *= f;
           }
         }
+      float ref[NT][2];  // a row that has seen nothing yet: all its scores are -inf
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int i = 0; i < 2; ++i) ref[nt][i] = m[nt][i] == -INFINITY ? 0.0f : m[nt][i];
+      score(ref);
     }
+    if (a.scores && t < 2) {
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+          for (int n = 0; n < 4; ++n)
+            a.scores[(static_cast<int64_t>(bh) * a.rows_pad + r0 + 4 * nt + 2 * t + i) * a.score_stride + tok0 + 8 * n] =
+                s[nt][i][n] + (m[nt][i] == -INFINITY ? 0.0f : m[nt][i]);
+    }
+
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const float base = m[nt][i] == -INFINITY ? 0.0f : m[nt][i];  // a row that has seen nothing yet
+      for (int i = 0; i < 2; ++i)
 #pragma unroll
         for (int n = 0; n < 4; ++n) {
-          s[nt][i][n] = ex2(s[nt][i][n] - base);
+          s[nt][i][n] = ex2(s[nt][i][n]);
           l[nt][i] += s[nt][i][n];
         }
-      }
 
     // V of contraction steps 2 t and 2 t + 1 (mt, half by half): channels 32 j + 4 g + 0..3
     uint32_t v[4][2][J / 2];
@@ -538,42 +589,41 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 4 : 2) kv_attention_ker
     }
 #pragma unroll
     for (int c = 0; c < NG; ++c) {
+      // p s is held as p s 2^(6 - e), where s < 2^(e + 1) as far as seen: below
+      // 2^15, for p is below 2^8. When an s is larger, e follows.
       float sv[4], lo[4];
-      uint32_t top_s = 0;  // bits of the largest scale, which has no sign
+      float f = __uint_as_float(static_cast<uint32_t>(260 - e_run[c]) << 23);
 #pragma unroll
       for (int n = 0; n < 4; ++n) {
-        const uint32_t w = mv[n][c];
-        sv[n] = pair_scale<BF>(w);
-        lo[n] = fmaf(sv[n], 8.0f, pair_low<BF>(w));
-        top_s = max(top_s, w & 0xFFFFu);
+        sv[n] = pair_scale<BF>(mv[n][c]);
+        lo[n] = fmaf(sv[n], 8.0f, pair_low<BF>(mv[n][c]));
       }
-      // p s is held as p s 2^(14 - e), e the exponent of the largest finite s so far
-      top_s = __reduce_max_sync(kFull, top_s);
-      constexpr uint32_t kInf = BF ? 0x7F80u : 0x7C00u;
-      if (top_s >= kInf) {
-        top_s = 0;
+      const float large = fmaxf(fmaxf(sv[0], sv[1]), fmaxf(sv[2], sv[3])) * f;
+      if (__any_sync(kFull, large >= 128.0f)) {
+        uint32_t top_s = 0;
 #pragma unroll
         for (int n = 0; n < 4; ++n) {
-          const uint32_t v = mv[n][c] & 0xFFFFu;
-          top_s = max(top_s, v < kInf ? v : 0u);
+          const uint32_t bits = __float_as_uint(fabsf(sv[n]));
+          top_s = max(top_s, bits < 0x7F800000u ? bits : 0u);
         }
-        top_s = __reduce_max_sync(kFull, top_s);
+        const int e_new = static_cast<int>(__reduce_max_sync(kFull, top_s) >> 23);
+        if (e_new > e_run[c]) {
+          const float down = e_new - e_run[c] > 126 ? 0.0f : pow2(e_run[c] - e_new);
+#pragma unroll
+          for (int j = c * JG; j < (c + 1) * JG; ++j)
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                o[j][0][nt][i] *= down;
+                o[j][1][nt][i] *= down;
+              }
+          e_run[c] = e_new;
+          f = __uint_as_float(static_cast<uint32_t>(260 - e_new) << 23);
+        }
       }
-      const int e_new = static_cast<int>(__float_as_uint(pair_scale<BF>(top_s)) >> 23);
-      if (e_new > e_run[c]) {
-        const float f = e_new - e_run[c] > 126 ? 0.0f : pow2(e_run[c] - e_new);
 #pragma unroll
-        for (int j = c * JG; j < (c + 1) * JG; ++j)
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              o[j][0][nt][i] *= f;
-              o[j][1][nt][i] *= f;
-            }
-        e_run[c] = e_new;
-      }
-      const float f = __uint_as_float(static_cast<uint32_t>(268 - e_run[c]) << 23);
+      for (int n = 0; n < 4; ++n) sv[n] *= f;
       uint32_t pf[NT][4];  // B fragments of both products, k = token
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
@@ -583,7 +633,7 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 4 : 2) kv_attention_ker
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
             const bool hidden = edge && tok0 + 8 * n >= lim[nt][i];  // 0 times a NaN that other rows see
-            x[i] = hidden ? 0.0f : s[nt][i][n] * (sv[n] * f);
+            x[i] = hidden ? 0.0f : s[nt][i][n] * sv[n];
             lsum[nt][i][c] += hidden ? 0.0f : s[nt][i][n] * lo[n];
             // columns 4..7 take what fp16's 11 bits, cut toward zero, leave
             x[i] -= __uint_as_float(__float_as_uint(x[i]) & rest_mask);
@@ -613,7 +663,8 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 4 : 2) kv_attention_ker
   }
   __syncthreads();  // every ring is idle: the sums take their place
 
-  // the warp's sums to shared memory, in natural units
+  // the warp's sums to shared memory, in natural units: columns 4..7 of four
+  // rows hold what their rounding left, and the lowest values' part is theirs too
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -624,129 +675,179 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 4 : 2) kv_attention_ker
 #pragma unroll
         for (int n = 0; n < NG; ++n) lsum[nt][i][n] += __shfl_xor_sync(kFull, lsum[nt][i][n], d);
       }
-      const int row = 4 * nt + 2 * t + i;
 #pragma unroll
       for (int j = 0; j < J; ++j) {
-        float x[4] = {o[j][0][nt][i], o[j][0][nt][2 + i] * 0.0625f, o[j][1][nt][i], o[j][1][nt][2 + i] * 0.0625f};
-        const float up = pow2(e_run[j / JG] - 127 - 14);
-#pragma unroll
-        for (int n = 0; n < 4; ++n) {
-          x[n] += __shfl_xor_sync(kFull, x[n], 2);  // the columns of the rounding's rest
-          x[n] = fmaf(x[n], up, lsum[nt][i][j / JG]);
-        }
-        if (t < 2) *reinterpret_cast<float4*>(&s_o[warp][row][32 * j + 4 * g]) = make_float4(x[0], x[1], x[2], x[3]);
+        const float up = pow2(e_run[j / JG] - 127 - 6), up16 = up * 0.0625f, low = t < 2 ? 0.0f : lsum[nt][i][j / JG];
+        *reinterpret_cast<float4*>(&s_o[warp][8 * nt + 2 * t + i][32 * j + 4 * g]) =
+            make_float4(fmaf(o[j][0][nt][i], up, low), fmaf(o[j][0][nt][2 + i], up16, low), fmaf(o[j][1][nt][i], up, low),
+                        fmaf(o[j][1][nt][2 + i], up16, low));
       }
       if (t < 2 && g == 0) {
-        s_m[warp][row] = m[nt][i];
-        s_l[warp][row] = l[nt][i];
+        s_m[warp][4 * nt + 2 * t + i] = m[nt][i];
+        s_l[warp][4 * nt + 2 * t + i] = l[nt][i];
       }
     }
   __syncthreads();
   const bool whole = n_rounds == rounds;
-  for (int idx = threadIdx.x; idx < ROWS * D; idx += kWarps * 32) {
-    const int row = idx / D, d = idx - row * D, r = r0 + row;
+  const bool direct = a.cluster == 0 ? whole : a.cluster == 1;
+  auto put = [&](int r, int d, float4 sum, float den) {  // 4 channels from d on
+    const int tok = r / a.per;
+    uint16_t* out = a.out + (static_cast<int64_t>(b) * a.n_new + tok) * a.out_stride + (h * a.per + r - tok * a.per) * D + d;
+    const float f = den == 0.0f ? 0.0f : 1.0f / den;
+    const uint16_t y[4] = {ops::store16(sum.x * f, BF), ops::store16(sum.y * f, BF), ops::store16(sum.z * f, BF), ops::store16(sum.w * f, BF)};
+    if (a.vec_out) {
+      *reinterpret_cast<uint2*>(out) = make_uint2(ops::pack2(y[0], y[1]), ops::pack2(y[2], y[3]));
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) out[i] = y[i];
+    }
+  };
+  for (int idx = threadIdx.x; idx < ROWS * D / 4; idx += kWarps * 32) {
+    const int row = idx / (D / 4), d = 4 * (idx - row * (D / 4)), r = r0 + row;
+    const int col = 8 * (row >> 2) + (row & 3);
     float top = s_m[0][row];
 #pragma unroll
     for (int w = 1; w < kWarps; ++w) top = fmaxf(top, s_m[w][row]);
     const float base = top == -INFINITY ? 0.0f : top;
-    float sum = 0.0f, den = 0.0f;
+    float4 sum = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    float den = 0.0f;
 #pragma unroll
     for (int w = 0; w < kWarps; ++w) {
       const float f = ex2(s_m[w][row] - base);
-      sum += f * s_o[w][row][d];
-      den += f * s_l[w][row];
+      const float4 hi = *reinterpret_cast<const float4*>(&s_o[w][col][d]), lo = *reinterpret_cast<const float4*>(&s_o[w][col + 4][d]);
+      sum.x = fmaf(f, hi.x + lo.x, sum.x);
+      sum.y = fmaf(f, hi.y + lo.y, sum.y);
+      sum.z = fmaf(f, hi.z + lo.z, sum.z);
+      sum.w = fmaf(f, hi.w + lo.w, sum.w);
+      den = fmaf(f, s_l[w][row], den);
     }
-    if (r >= a.rows) continue;
-    if (whole) {
-      const int tok = r / a.per;
-      a.out[(static_cast<int64_t>(b) * a.n_new + tok) * a.out_stride + (h * a.per + r - tok * a.per) * D + d] =
-          ops::store16(den == 0.0f ? 0.0f : sum / den, BF);
-      if (a.scores && d == 0) a.unit_ml[static_cast<int64_t>(bh) * a.rows_pad + r] = make_float2(top, den);
-    } else {
-      const int64_t slot = (2 * static_cast<int64_t>(blockIdx.x) + (first_segment ? 0 : 1)) * ROWS + row;
-      a.part_o[slot * D + d] = sum;
+    if (direct) {
+      if (r < a.rows) {
+        put(r, d, sum, den);
+        if (a.scores && d == 0) a.unit_ml[static_cast<int64_t>(bh) * a.rows_pad + r] = make_float2(top, den);
+      }
+    } else if (a.cluster == 0) {
+      const int slot = (2 * blockIdx.x + (first_segment ? 0 : 1)) * ROWS + row;
+      *reinterpret_cast<float4*>(a.part_o + static_cast<int64_t>(slot) * D + d) = sum;
       if (d == 0) a.part_ml[slot] = make_float2(top, den);
+    } else {
+      *reinterpret_cast<float4*>(&s_o[0][col][d]) = sum;  // this thread alone reads and writes these elements
+      if (d == 0) {
+        s_top[row] = top;
+        s_den[row] = den;
+      }
     }
+  }
+  if (a.cluster > 1) {
+    cluster_sync_all();
+    const uint32_t o_addr = kernels::smem_addr(&s_o[0][0][0]), top_addr = kernels::smem_addr(s_top), den_addr = kernels::smem_addr(s_den);
+    for (int idx = threadIdx.x * a.cluster + part; idx < ROWS * D / 4; idx += a.cluster * kWarps * 32) {
+      const int row = idx / (D / 4), d = 4 * (idx - row * (D / 4));
+      if (r0 + row >= a.rows) continue;
+      const uint32_t at_o = o_addr + 4 * ((8 * (row >> 2) + (row & 3)) * D + d);
+      float m_p[kMaxCluster], l_p[kMaxCluster], top = -INFINITY;
+      float4 o_p[kMaxCluster];
+#pragma unroll
+      for (int c = 0; c < kMaxCluster; ++c) {
+        m_p[c] = -INFINITY;
+        l_p[c] = 0.0f;
+        o_p[c] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        if (c < a.cluster) {
+          m_p[c] = load_peer(top_addr + 4 * row, c);
+          l_p[c] = load_peer(den_addr + 4 * row, c);
+          o_p[c] = load_peer4(at_o, c);
+        }
+        top = fmaxf(top, m_p[c]);
+      }
+      const float base = top == -INFINITY ? 0.0f : top;
+      float4 sum = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+      float den = 0.0f;
+#pragma unroll
+      for (int c = 0; c < kMaxCluster; ++c) {
+        const float f = ex2(m_p[c] - base);
+        sum.x = fmaf(f, o_p[c].x, sum.x);
+        sum.y = fmaf(f, o_p[c].y, sum.y);
+        sum.z = fmaf(f, o_p[c].z, sum.z);
+        sum.w = fmaf(f, o_p[c].w, sum.w);
+        den = fmaf(f, l_p[c], den);
+      }
+      put(r0 + row, d, sum, den);
+    }
+    cluster_sync_all();  // no CTA leaves while a peer reads its sums
+    return;
   }
   asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // bulk copies will overwrite what was read here
   __syncthreads();
   }
 }
 
-// The partial sums of unit `unit` of sequence b: those of CTAs first .. last,
-// the first's in slot `slot` and the others' in slot 0. False if one CTA wrote
-// the unit out (or there is none).
-struct Parts {
-  int first, last, slot;
-};
-__device__ __forceinline__ bool parts_of(const KvAttnArgs& a, int b, int unit, int lane, Parts& p) {
-  const int rounds = rounds_of(a, b);
-  if (rounds == 0) return false;
-  const int units_b = a.kv.heads * a.row_blocks;
-  const int64_t total = rounds_before(a, a.batch, lane) * units_b;
-  const int64_t lo = rounds_before(a, b, lane) * units_b + static_cast<int64_t>(unit) * rounds, hi = lo + rounds;
-  const int busy = busy_ctas(total, a.ctas);
-  // CTA c holds round x if run_start(c) <= x < run_start(c + 1): the largest c with total c / busy < x + 1
-  auto holder = [&](int64_t x) { return static_cast<int>(((x + 1) * busy - 1) / total); };
-  p.first = holder(lo);
-  p.last = holder(hi - 1);
-  if (p.first == p.last) return false;
-  // slot 0 if the unit is the first that the CTA works on
-  p.slot = run_start(total, p.first, busy) >= lo ? 0 : 1;
-  return true;
-}
-
-// Joins the partial sums: CTAs before `n_units` each write the output rows of a
-// unit; the others (tracked calls) add the weights exp2(S - lse) of 512 tokens
-// of one (sequence, head) to the mass, every element by one thread in one
-// order.
+// Joins the partial sums: CTAs before n_units * ROWS each write one output row;
+// the others (tracked calls) add the weights exp2(S - lse) of 512 tokens of one
+// (sequence, head) to the mass, every element by one thread in one order.
 template <int D, int ROWS>
 __global__ void __launch_bounds__(512) kv_join_kernel(const __grid_constant__ KvAttnArgs a) {
   constexpr int GROUPS = 512 / D;  // partial sums read at a time
-  __shared__ float s_sum[GROUPS][D];
+  __shared__ float s_sum[GROUPS][D], s_top[GROUPS], s_den[GROUPS];
   __shared__ float s_lse[STAGQ_KV_MAX_NEW * STAGQ_KV_MAX_SHARE];
   grid_launch_dependents();
   grid_dependency_wait();
   const KvView& kv = a.kv;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int n_units = a.batch * kv.heads * a.row_blocks;
-  // a row's maximum, and its denominator, over the partial sums of its unit
-  auto row_sum = [&](const Parts& p, int row, float& top, float& den) {
-    top = -INFINITY;
-    for (int c = p.first + lane; c <= p.last; c += 32)
-      top = fmaxf(top, a.part_ml[(2 * static_cast<int64_t>(c) + (c == p.first ? p.slot : 0)) * ROWS + row].x);
-#pragma unroll
-    for (int d = 1; d < 32; d <<= 1) top = fmaxf(top, __shfl_xor_sync(kFull, top, d));
-    const float base = top == -INFINITY ? 0.0f : top;
-    den = 0.0f;
-    for (int c = p.first + lane; c <= p.last; c += 32) {
-      const float2 ml = a.part_ml[(2 * static_cast<int64_t>(c) + (c == p.first ? p.slot : 0)) * ROWS + row];
-      den += ex2(ml.x - base) * ml.y;
-    }
-#pragma unroll
-    for (int d = 1; d < 32; d <<= 1) den += __shfl_xor_sync(kFull, den, d);
-  };
-  Parts p;
+  const int units_b = kv.heads * a.row_blocks, n_units = a.batch * units_b;
+  // slot of row `row` in CTA c's partial sum of a unit
+  auto slot_of = [&](const int4& p, int c, int row) { return (2 * c + (c == p.x ? p.z : 0)) * ROWS + row; };
   if (static_cast<int64_t>(blockIdx.x) < static_cast<int64_t>(n_units) * ROWS) {
     const int u = blockIdx.x / ROWS, row = blockIdx.x - u * ROWS;
-    const int b = u / (kv.heads * a.row_blocks), unit = u - b * kv.heads * a.row_blocks;
+    const int b = u / units_b, unit = u - b * units_b;
     const int h = unit / a.row_blocks, r = (unit - h * a.row_blocks) * ROWS + row;
-    if (r >= a.rows || !parts_of(a, b, unit, lane, p)) return;
-    float top, den;
-    row_sum(p, row, top, den);
-    const float base = top == -INFINITY ? 0.0f : top;
+    if (r >= a.rows || a.lens[b] <= 0) return;
+    const int4 p = a.parts[u];
+    if (p.x == p.y) return;  // one CTA wrote the unit out
     const int group = threadIdx.x / D, d = threadIdx.x - group * D;
-    float sum = 0.0f;
-#pragma unroll 4
-    for (int c = p.first + group; c <= p.last; c += GROUPS) {
-      const int64_t slot = (2 * static_cast<int64_t>(c) + (c == p.first ? p.slot : 0)) * ROWS + row;
-      sum += ex2(a.part_ml[slot].x - base) * a.part_o[slot * D + d];
+    float top = -INFINITY, den = 0.0f, sum = 0.0f;
+    for (int c0 = p.x + group; c0 <= p.y; c0 += 4 * GROUPS) {
+      float2 ml[4];
+      float o[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int c = c0 + i * GROUPS;
+        ml[i] = make_float2(-INFINITY, 0.0f);
+        o[i] = 0.0f;
+        if (c <= p.y) {
+          const int slot = slot_of(p, c, row);
+          ml[i] = a.part_ml[slot];
+          o[i] = a.part_o[static_cast<int64_t>(slot) * D + d];
+        }
+      }
+      const float now = fmaxf(fmaxf(fmaxf(ml[0].x, ml[1].x), fmaxf(ml[2].x, ml[3].x)), top);
+      const float base = now == -INFINITY ? 0.0f : now, f = ex2(top - base);
+      sum *= f;
+      den *= f;
+      top = now;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float w = ex2(ml[i].x - base);
+        sum += w * o[i];
+        den += w * ml[i].y;
+      }
     }
     s_sum[group][d] = sum;
+    if (d == 0) {
+      s_top[group] = top;
+      s_den[group] = den;
+    }
     __syncthreads();
     if (threadIdx.x >= D) return;
+    top = s_top[0];
 #pragma unroll
-    for (int i = 1; i < GROUPS; ++i) sum += s_sum[i][d];
+    for (int i = 1; i < GROUPS; ++i) top = fmaxf(top, s_top[i]);
+    const float base = top == -INFINITY ? 0.0f : top;
+    sum = den = 0.0f;
+#pragma unroll
+    for (int i = 0; i < GROUPS; ++i) {
+      const float w = ex2(s_top[i] - base);
+      sum += w * s_sum[i][d];
+      den += w * s_den[i];
+    }
     const int tok = r / a.per;
     a.out[(static_cast<int64_t>(b) * a.n_new + tok) * a.out_stride + (h * a.per + r - tok * a.per) * D + d] =
         ops::store16(den == 0.0f ? 0.0f : sum / den, kv.bf16);
@@ -758,28 +859,52 @@ __global__ void __launch_bounds__(512) kv_join_kernel(const __grid_constant__ Kv
   const int b = bh / kv.heads, h = bh - b * kv.heads;
   const int len = clamped_len(a, b);
   if (tok - static_cast<int>(threadIdx.x) >= len) return;
-  for (int rb = 0; rb < a.row_blocks; ++rb) {
-    const bool parts = parts_of(a, b, h * a.row_blocks + rb, lane, p);
-    for (int row = warp; row < ROWS && rb * ROWS + row < a.rows; row += 16) {
-      float top, den;
-      if (parts) {
-        row_sum(p, row, top, den);
-      } else {
-        const float2 ml = a.unit_ml[static_cast<int64_t>(bh) * a.rows_pad + rb * ROWS + row];
-        top = ml.x;
-        den = ml.y;
+  // the scores of the first rows load while their denominators are found
+  const float* scores = a.scores + static_cast<int64_t>(bh) * a.rows_pad * a.score_stride + tok;
+  constexpr int EARLY = 8;
+  float early[EARLY];
+#pragma unroll
+  for (int r = 0; r < EARLY; ++r) early[r] = r < a.rows && tok < row_limit(a, len, r) ? scores[r * a.score_stride] : -INFINITY;
+  float old = 0.0f;
+  float* mass = a.mass + b * a.mass_stride_b + h * a.mass_stride_h + tok;
+  if (tok < len) old = *mass;
+  const int lane = threadIdx.x & 31;
+  for (int r = threadIdx.x >> 5; r < a.rows; r += 16) {
+    const int rb = r / ROWS, row = r - rb * ROWS;
+    const int4 p = a.parts[b * units_b + h * a.row_blocks + rb];
+    float top, den;
+    if (p.x == p.y) {
+      const float2 ml = a.unit_ml[static_cast<int64_t>(bh) * a.rows_pad + r];
+      top = ml.x;
+      den = ml.y;
+    } else {
+      top = -INFINITY;
+      den = 0.0f;
+      for (int c = p.x + lane; c <= p.y; c += 32) {
+        const float2 ml = a.part_ml[slot_of(p, c, row)];
+        const float now = fmaxf(top, ml.x), base = now == -INFINITY ? 0.0f : now;
+        den = den * ex2(top - base) + ml.y * ex2(ml.x - base);
+        top = now;
       }
-      if (lane == 0) s_lse[rb * ROWS + row] = (top == -INFINITY ? 0.0f : top) + log2f(den);
+#pragma unroll
+      for (int d = 1; d < 32; d <<= 1) {
+        const float t2 = __shfl_xor_sync(kFull, top, d), d2 = __shfl_xor_sync(kFull, den, d);
+        const float now = fmaxf(top, t2), base = now == -INFINITY ? 0.0f : now;
+        den = den * ex2(top - base) + d2 * ex2(t2 - base);
+        top = now;
+      }
     }
+    if (lane == 0) s_lse[r] = (top == -INFINITY ? 0.0f : top) + log2f(den);
   }
   __syncthreads();
   if (tok >= len) return;
-  const float* scores = a.scores + static_cast<int64_t>(bh) * a.rows_pad * a.score_stride + tok;
   float sum = 0.0f;
-#pragma unroll 4
-  for (int r = 0; r < a.rows; ++r)
+#pragma unroll
+  for (int r = 0; r < EARLY; ++r)
+    if (r < a.rows && tok < row_limit(a, len, r)) sum += ex2(early[r] - s_lse[r]);
+  for (int r = EARLY; r < a.rows; ++r)
     if (tok < row_limit(a, len, r)) sum += ex2(scores[r * a.score_stride] - s_lse[r]);
-  a.mass[b * a.mass_stride_b + h * a.mass_stride_h + tok] += sum;
+  *mass = old + sum;
 }
 
 template <int D, int NG, int NT, bool BF>
@@ -787,7 +912,20 @@ cudaError_t launch_attention(const KvAttnArgs& a, cudaStream_t s) {
   constexpr int smem = kWarps * kStages * TileLayout<D, NG>::kBytes;
   cudaError_t e = cudaFuncSetAttribute(kv_attention_kernel<D, NG, NT, BF>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
-  e = launch_op(kv_attention_kernel<D, NG, NT, BF>, dim3(a.ctas), dim3(kWarps * 32), smem, s, a);
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(a.ctas);
+  cfg.blockDim = dim3(kWarps * 32);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = a.cluster > 1 ? a.cluster : 1;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  e = cudaLaunchKernelEx(&cfg, kv_attention_kernel<D, NG, NT, BF>, a);
   if (e != cudaSuccess || !a.part_o) return e;
   int64_t join = static_cast<int64_t>(a.batch) * a.kv.heads * a.row_blocks * 4 * NT;
   if (a.scores) join += static_cast<int64_t>(a.batch) * a.kv.heads * ((a.max_len + 511) / 512);
@@ -805,9 +943,14 @@ int64_t align256(int64_t v) { return (v + 255) / 256 * 256; }
 }  // namespace
 
 // Four query rows of a KV head per unit, eight where there are more than four
-// (the cache is then read once per eight rows). As many CTAs as fit the GPU at
-// once, but no more than there can be rounds. Units of one round need no join.
-KvAttnPlan plan_kv_attention(int batch, int heads, int q_heads, int n_new, int dim, int max_len, bool mass,
+// (the cache is then read once per eight rows). A round takes about 1 us in a
+// CTA that has its SM to itself and 4 us where all of them are full. Clusters
+// of S CTAs per unit (S up to 8, no more than the rounds, all resident at once
+// where that goes) take ceil(rounds / S) rounds after one another, of the
+// longest sequence; the even split takes an equal share of all rounds (of a
+// batch, about 0.6 times the longest sequence's each), and a second launch of
+// about 5 us.
+KvAttnPlan plan_kv_attention(int batch, int heads, int q_heads, int n_new, int dim, int group, int max_len, bool mass,
                              int num_sms) {
   KvAttnPlan p{};
   const int rows = q_heads / heads * n_new;
@@ -816,18 +959,28 @@ KvAttnPlan plan_kv_attention(int batch, int heads, int q_heads, int n_new, int d
   p.rows_pad = p.row_blocks * 4 * p.nt;
   const int64_t units = static_cast<int64_t>(batch) * heads * p.row_blocks;
   const int64_t rounds = (static_cast<int64_t>(max_len) + kWarps * kTile - 1) / (kWarps * kTile);
-  const int64_t fit = static_cast<int64_t>(num_sms) * (p.nt == 1 ? 4 : 2);
+  const int64_t fit = static_cast<int64_t>(num_sms) * resident_ctas(p.nt, dim / group);
   p.score_stride = mass ? rounds * kWarps * kTile : 0;
-  if (rounds == 1 && !mass) {
-    p.ctas = static_cast<int>(units);
-    return p;
+  if (!mass) {
+    int64_t s = 1;
+    while (s < kMaxCluster && s < rounds && units * s * 2 <= fit) s *= 2;
+    auto round_us = [&](int64_t ctas) { return ctas >= fit ? 4.0 : ctas * 4 <= fit ? 1.0 : 4.0 * ctas / fit; };
+    const double waves = static_cast<double>((units * s + fit - 1) / fit);
+    const double clusters_us = waves * static_cast<double>((rounds + s - 1) / s) * round_us(units * s);
+    const double work = static_cast<double>(units * rounds) * (batch > 1 ? 0.6 : 1.0);
+    const double even_us = std::ceil(work / fit) * round_us(units * rounds) + 5.0;
+    if (rounds == 1 || clusters_us <= even_us) {
+      p.cluster = static_cast<int>(s);
+      p.ctas = static_cast<int>(units * s);
+      return p;
+    }
   }
   p.ctas = static_cast<int>(units * rounds < fit ? units * rounds : fit);
   const int64_t slots = 2 * static_cast<int64_t>(p.ctas) * 4 * p.nt;
-  p.off_ml = 0;
-  p.off_o = align256(slots * 8);
-  p.off_unit = p.off_o + align256(slots * dim * 4);
   const int64_t rows_all = static_cast<int64_t>(batch) * heads * p.rows_pad;
+  p.off_ml = align256(units * 16);  // the units' parts come first
+  p.off_o = p.off_ml + align256(slots * 8);
+  p.off_unit = p.off_o + align256(slots * dim * 4);
   p.off_scores = p.off_unit + (mass ? align256(rows_all * 8) : 0);
   p.bytes = p.off_scores + align256(rows_all * p.score_stride * 4);
   return p;

@@ -40,12 +40,14 @@ struct KvAttnArgs {
   const int32_t* lens;
   float* mass;             // null: not tracked
   int64_t mass_stride_b, mass_stride_h;
+  int4* parts;             // by unit: first and last CTA with a part of it, the first's slot
   float* part_o;           // partial sums: [ctas][2][rows of a block][dim]; null: no unit is shared
   float2* part_ml;         // their maxima and denominators
   float2* unit_ml;         // tracked: the same of the rows that one CTA finished, [batch * heads][rows_pad]
   float* scores;           // [batch * heads][rows_pad][score_stride]
   int64_t score_stride;
-  int32_t batch, q_heads, per, n_new, rows, rows_pad, row_blocks, ctas, max_len, vec;
+  int32_t batch, q_heads, per, n_new, rows, rows_pad, row_blocks, ctas, max_len, vec_out;
+  int32_t cluster;         // CTAs per unit, or 0: the even split
   float scale_log2;        // softmax scale times log2(e)
 };
 
@@ -62,12 +64,12 @@ struct KvEvictArgs {
 
 struct KvAttnPlan {
   int nt;                  // query rows per CTA: 4 * nt
-  int row_blocks, ctas, rows_pad;
+  int row_blocks, ctas, rows_pad, cluster;
   int64_t score_stride;
   int64_t off_ml, off_o, off_unit, off_scores, bytes;  // workspace layout
 };
 
-KvAttnPlan plan_kv_attention(int batch, int heads, int q_heads, int n_new, int dim, int max_len, bool mass,
+KvAttnPlan plan_kv_attention(int batch, int heads, int q_heads, int n_new, int dim, int group, int max_len, bool mass,
                              int num_sms);
 
 cudaError_t launch_kv_append(const KvRowsArgs& a, cudaStream_t s);

@@ -227,8 +227,8 @@ const char* attention_error(const stagq_kv_cache* c, int32_t batch, int32_t max_
   // the join's grid: rows in blocks of up to 8, and 512 tokens of a head per CTA
   const int64_t heads = static_cast<int64_t>(batch) * c->heads;
   if (heads * (q_heads / c->heads * n_new + 8 + (static_cast<int64_t>(max_len) + 511) / 512) > INT_MAX) return "too many rows for one call";
-  // rounds times CTAs, and scores, in 64 bits
-  if (heads * (q_heads / c->heads * n_new + 8) > (static_cast<int64_t>(1) << 58) / (static_cast<int64_t>(max_len) + 128) / 4) return "too many rows for one call";
+  // rounds of 128 tokens, numbered through all units
+  if (heads * (q_heads / c->heads * n_new + 8) > INT_MAX / ((static_cast<int64_t>(max_len) + 127) / 128 + 8)) return "too many rows for one call";
   return nullptr;
 }
 
@@ -245,7 +245,7 @@ extern "C" int64_t stagq_kv_attention_workspace(const stagq_kv_cache* c, int32_t
     set_error("no usable device");
     return -1;
   }
-  return plan_kv_attention(batch, c->heads, q_heads, n_new, c->dim, max_len, tracked != 0, sms).bytes;
+  return plan_kv_attention(batch, c->heads, q_heads, n_new, c->dim, c->group, max_len, tracked != 0, sms).bytes;
 }
 
 extern "C" int stagq_kv_attention(const stagq_kv_cache* c, const stagq_kv_table* t, const int32_t* lens,
@@ -266,7 +266,7 @@ extern "C" int stagq_kv_attention(const stagq_kv_cache* c, const stagq_kv_table*
   if (!guard.ok) return fail(STAGQ_ECUDA, "cudaSetDevice failed");
   const int sms = sm_count(c->device);
   if (!sms) return fail(STAGQ_ENODEV, "no usable device");
-  const KvAttnPlan p = plan_kv_attention(t->batch, c->heads, q_heads, n_new, c->dim, max_len, mass != nullptr, sms);
+  const KvAttnPlan p = plan_kv_attention(t->batch, c->heads, q_heads, n_new, c->dim, c->group, max_len, mass != nullptr, sms);
   if (p.bytes && (!workspace || !aligned(workspace, 256) || workspace_bytes < p.bytes))
     return bad("workspace must be 256-byte aligned and hold stagq_kv_attention_workspace() bytes");
   KvAttnArgs a{};
@@ -281,6 +281,7 @@ extern "C" int stagq_kv_attention(const stagq_kv_cache* c, const stagq_kv_table*
   a.mass_stride_h = mass_stride_h;
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   if (p.bytes) {
+    a.parts = reinterpret_cast<int4*>(ws);
     a.part_ml = reinterpret_cast<float2*>(ws + p.off_ml);
     a.part_o = reinterpret_cast<float*>(ws + p.off_o);
     if (mass) {
@@ -297,8 +298,9 @@ extern "C" int stagq_kv_attention(const stagq_kv_cache* c, const stagq_kv_table*
   a.rows_pad = p.rows_pad;
   a.row_blocks = p.row_blocks;
   a.ctas = p.ctas;
+  a.cluster = p.cluster;
   a.max_len = max_len;
-  a.vec = wide(q, q_stride, 2);
+  a.vec_out = aligned(out, 8) && out_stride % 4 == 0;
   a.scale_log2 = scale * 1.4426950408889634f;
   return launched(launch_kv_attention(a, p, static_cast<cudaStream_t>(cuda_stream)), "attention launch");
 }

@@ -487,13 +487,23 @@ def test_attention_takes_slices_other_streams_and_workspaces():
     q = qkv[:, 3:3 + 8 * 128]                                           # rows not on 16 bytes
     want = c.check(8, 1, q=q.cpu().contiguous())
     whole = torch.full((2, 2000), 3.0, dtype=F16, device="cuda")
-    need = Q.stagq_kv_attention_workspace(c.cache, 2, c.width * 32, 8)
-    assert need > 0
+    need = Q.stagq_kv_attention_workspace(c.cache, 2, c.width * 32, 8, tracked=True)
+    mass = torch.zeros(2, 2, c.width * 32, device="cuda")
     with pytest.raises(Q.StagqError):
-        Q.stagq_kv_attention(c.cache, q, c.table, c.lens, whole[:, 5:1029], workspace=torch.empty(need - 1, dtype=torch.uint8, device="cuda"))
+        Q.stagq_kv_attention(c.cache, q, c.table, c.lens, whole[:, 5:1029], mass=mass, workspace=torch.empty(need - 1, dtype=torch.uint8, device="cuda"))
     s = torch.cuda.Stream()
     s.wait_stream(torch.cuda.current_stream())
-    Q.stagq_kv_attention(c.cache, q, c.table, c.lens, whole[:, 5:1029], workspace=torch.empty(need, dtype=torch.uint8, device="cuda"), stream=s)
+    Q.stagq_kv_attention(c.cache, q, c.table, c.lens, whole[:, 5:1029], stream=s)
+    s.synchronize()
+    assert torch.equal(whole[:, 5:1029], want)
+    whole.fill_(3.0)
+    s.wait_stream(torch.cuda.current_stream())
+    ws = torch.empty(need, dtype=torch.uint8, device="cuda")
+    Q.stagq_kv_attention(c.cache, q, c.table, c.lens, whole[:, 5:1029], mass=mass, workspace=ws, stream=s)
+    s.synchronize()
+    out, _, bound, _ = R.attention(q.cpu().reshape(2, 1, 8, 128), c.k, c.v, c.lens_l, 1, 128 ** -0.5)
+    assert_rounded(whole[:, 5:1029].reshape(out.shape), out, F16, bound[..., None])
+    want = whole[:, 5:1029].clone()
     s.synchronize()
     assert torch.equal(whole[:, 5:1029], want)
     assert (whole[:, :5] == 3).all() and (whole[:, 1029:] == 3).all()
