@@ -496,21 +496,20 @@ def stagq_free(m: Matrix) -> None:
 
 # ------------------------------------------------------- operators beside the GEMV
 
-# A call of these operators takes microseconds on the GPU, so the checks below
-# look at each tensor once and the shapes of a cache are checked when it is made.
+# A call of these operators takes microseconds on the GPU. The checks of a
+# tensor that fits are therefore one expression; what is wrong with one that
+# does not is found out afterwards.
 
-_SIXTEEN = ("float16", "bfloat16")
 _tensor_type = None
-_dtype_names = {}
+_F16 = _BF16 = _F32 = _I8 = _U8 = _I32 = None
 _raw_stream = None
 
 
-def _torch_names() -> None:
+def _bind_torch() -> None:
     """Binds what the checks need of torch, on the first call of an operator."""
-    global _tensor_type, _raw_stream
+    global _tensor_type, _raw_stream, _F16, _BF16, _F32, _I8, _U8, _I32
     import torch
-    for name in ("float16", "bfloat16", "float32", "int8", "uint8", "int32"):
-        _dtype_names[getattr(torch, name)] = name
+    _F16, _BF16, _F32, _I8, _U8, _I32 = (torch.float16, torch.bfloat16, torch.float32, torch.int8, torch.uint8, torch.int32)
     _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
         (lambda device: torch.cuda.current_stream(device).cuda_stream)
     _tensor_type = torch.Tensor
@@ -525,7 +524,7 @@ def _op_stream(stream, device: int) -> int:
 
 def _cuda_index(t, name: str) -> int:
     if _tensor_type is None:
-        _torch_names()
+        _bind_torch()
     if not isinstance(t, _tensor_type):
         raise TypeError(f"{name} must be a torch tensor")
     device = t.get_device()
@@ -534,39 +533,39 @@ def _cuda_index(t, name: str) -> int:
     return device
 
 
-def _check_op(t, name: str, dtypes, device: int) -> str:
-    """The name of t's dtype, one of `dtypes`; t is a CUDA tensor of `device`."""
+def _refuse(t, name: str, dtypes, device: int, shape, contiguous: bool):
+    """Raises for a tensor that does not fit."""
     if not isinstance(t, _tensor_type):
         raise TypeError(f"{name} must be a torch tensor")
-    dtype = _dtype_names.get(t.dtype)
-    if dtype not in dtypes:
-        raise TypeError(f"{name} must be {' or '.join(dtypes)}, got {t.dtype}")
+    if t.dtype not in dtypes:
+        raise TypeError(f"{name} must be {' or '.join(str(d)[6:] for d in dtypes)}, got {t.dtype}")
     if t.get_device() != device:
         raise ValueError(f"{name} must be on cuda:{device} (the call's GPU), got {t.device}")
-    return dtype
-
-
-def _check_rows(t, name: str, rows: int, cols: int, dtypes, device: int):
-    """t is [rows, cols] with unit stride along a row; rows may lie further
-    apart. Returns the name of its dtype and the elements between two rows (a
-    single row's own length)."""
-    dtype = _check_op(t, name, dtypes, device)
-    if tuple(t.shape) != (rows, cols):
-        raise ValueError(f"{name} must be [{rows}, {cols}], got {list(t.shape)}")
-    row, col = t.stride()
-    if (cols > 1 and col != 1) or (rows > 1 and row < cols):
-        raise ValueError(f"{name} must have unit stride along its rows, which must not overlap")
-    return dtype, row if rows > 1 else cols
-
-
-def _check_flat(t, name: str, shape, dtype: str, device: int) -> None:
-    _check_op(t, name, (dtype,), device)
-    if tuple(t.shape) != shape:
+    if shape is not None and tuple(t.shape) != tuple(shape):
         raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
-    if not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
+    raise ValueError(f"{name} must be contiguous" if contiguous else
+                     f"{name} must have unit stride along its rows, which must not overlap")
 
 
+def _check_flat(t, name: str, shape, dtype, device: int) -> int:
+    """t's address; t is contiguous, of `shape` and `dtype`, on `device`."""
+    if not (isinstance(t, _tensor_type) and t.dtype is dtype and t.get_device() == device and t.shape == shape and
+            t.is_contiguous()):
+        _refuse(t, name, (dtype,), device, shape, True)
+    return t.data_ptr()
+
+
+def _check_rows(t, name: str, rows: int, cols: int, dtypes, device: int) -> int:
+    """The elements between two rows of t [rows, cols], which has unit stride
+    along a row (a single row's own length)."""
+    if isinstance(t, _tensor_type) and t.dtype in dtypes and t.get_device() == device and t.shape == (rows, cols):
+        row, col = t.stride()
+        if (col == 1 or cols == 1) and (row >= cols or rows == 1):
+            return row if rows > 1 else cols
+    _refuse(t, name, dtypes, device, (rows, cols), False)
+
+
+@functools.lru_cache(maxsize=None)
 def stagq_i8_row_bytes(inp: int) -> int:
     """Bytes of a row of `inp` 8-bit values: rows are padded with zeros to 128 bytes."""
     n = int(lib().stagq_i8_row_bytes(inp))
@@ -583,11 +582,11 @@ def stagq_quantize_i8(x, q, scale, stream=None) -> None:
     if x.dim() != 2:
         raise ValueError(f"x must be [n, inp], got {list(x.shape)}")
     n, inp = x.shape
-    dtype, stride = _check_rows(x, "x", n, inp, _SIXTEEN, dev)
-    _check_flat(q, "q", (n, stagq_i8_row_bytes(inp)), "int8", dev)
-    _check_flat(scale, "scale", (n,), "float32", dev)
-    _check(lib().stagq_quantize_i8(x.data_ptr(), stride, n, inp, STAGQ_BF16 if dtype == "bfloat16" else 0,
-                                   q.data_ptr(), scale.data_ptr(), dev, _op_stream(stream, dev)), "stagq_quantize_i8")
+    stride = _check_rows(x, "x", n, inp, (_F16, _BF16), dev)
+    _check(lib().stagq_quantize_i8(x.data_ptr(), stride, n, inp, STAGQ_BF16 if x.dtype is _BF16 else 0,
+                                   _check_flat(q, "q", (n, stagq_i8_row_bytes(inp)), _I8, dev),
+                                   _check_flat(scale, "scale", (n,), _F32, dev), dev, _op_stream(stream, dev)),
+           "stagq_quantize_i8")
 
 
 def stagq_gemm_i8(xq, xscale, wq, wscale, inp: int, y, stream=None) -> None:
@@ -595,15 +594,14 @@ def stagq_gemm_i8(xq, xscale, wq, wscale, inp: int, y, stream=None) -> None:
     xq int8 [n, row bytes] and wq int8 [out, row bytes] as stagq_quantize_i8
     leaves them, y [n, out] in fp16, bf16 or fp32."""
     dev = _cuda_index(xq, "xq")
+    _cuda_index(wq, "wq")
     n, out, row = xq.shape[0], wq.shape[0], stagq_i8_row_bytes(inp)
-    _check_flat(xq, "xq", (n, row), "int8", dev)
-    _check_flat(wq, "wq", (out, row), "int8", dev)
-    _check_flat(xscale, "xscale", (n,), "float32", dev)
-    _check_flat(wscale, "wscale", (out,), "float32", dev)
-    dtype, stride = _check_rows(y, "y", n, out, ("float16", "bfloat16", "float32"), dev)
-    flags = STAGQ_Y_F32 if dtype == "float32" else STAGQ_BF16 if dtype == "bfloat16" else 0
-    _check(lib().stagq_gemm_i8(xq.data_ptr(), xscale.data_ptr(), n, wq.data_ptr(), wscale.data_ptr(), out, inp,
-                               y.data_ptr(), stride, flags, dev, _op_stream(stream, dev)), "stagq_gemm_i8")
+    stride = _check_rows(y, "y", n, out, (_F16, _BF16, _F32), dev)
+    flags = 0 if y.dtype is _F16 else STAGQ_BF16 if y.dtype is _BF16 else STAGQ_Y_F32
+    _check(lib().stagq_gemm_i8(_check_flat(xq, "xq", (n, row), _I8, dev), _check_flat(xscale, "xscale", (n,), _F32, dev), n,
+                               _check_flat(wq, "wq", (out, row), _I8, dev),
+                               _check_flat(wscale, "wscale", (out,), _F32, dev), out, inp, y.data_ptr(), stride, flags, dev,
+                               _op_stream(stream, dev)), "stagq_gemm_i8")
 
 
 @functools.lru_cache(maxsize=None)
@@ -623,32 +621,34 @@ class KVCache:
     def __init__(self, pages, heads: int, dim: int, page: int, group: int, dtype):
         self.page_bytes = stagq_kv_page_bytes(heads, dim, page, group)
         self.device = _cuda_index(pages, "pages")
-        _check_op(pages, "pages", ("uint8",), self.device)
+        if pages.dtype is not _U8:
+            raise TypeError(f"pages must be uint8, got {pages.dtype}")
         if not pages.is_contiguous():
             raise ValueError("pages must be contiguous")
-        if pages.numel() < self.page_bytes or pages.numel() % self.page_bytes:
-            raise ValueError(f"pages holds {pages.numel()} bytes, not a multiple of a page's {self.page_bytes}")
-        self.dtype = _dtype_names.get(dtype)
-        if self.dtype not in _SIXTEEN:
+        size = pages.numel()
+        if size < self.page_bytes or size % self.page_bytes:
+            raise ValueError(f"pages holds {size} bytes, not a multiple of a page's {self.page_bytes}")
+        if dtype is not _F16 and dtype is not _BF16:
             raise TypeError(f"a cache is float16 or bfloat16, got {dtype}")
-        self.pages, self.heads, self.dim, self.page, self.group = pages, heads, dim, page, group
-        self._types = (self.dtype,)
-        self._row = heads * dim
-        self._c = _KvCache(pages.data_ptr(), pages.numel() // self.page_bytes, heads, dim, page, group,
-                           STAGQ_BF16 if self.dtype == "bfloat16" else 0, self.device)
+        self.pages, self.heads, self.dim, self.page, self.group, self.dtype = pages, heads, dim, page, group, dtype
+        self._types, self._row, self._workspace = (dtype,), heads * dim, {}  # the last: sizes by shape
+        self._c = _KvCache(pages.data_ptr(), size // self.page_bytes, heads, dim, page, group,
+                           STAGQ_BF16 if dtype is _BF16 else 0, self.device)
 
     def _table(self, table, name: str = "table") -> _KvTable:
-        _check_op(table, name, ("int32",), self.device)
-        if table.dim() != 2 or 0 in table.shape:
-            raise ValueError(f"{name} must be [batch, pages of a sequence], got {list(table.shape)}")
-        (batch, width), (row, col) = table.shape, table.stride()
-        if (width > 1 and col != 1) or (batch > 1 and row < width):
-            raise ValueError(f"{name} must have unit stride along its rows, which must not overlap")
-        return _KvTable(table.data_ptr(), row if batch > 1 else width, batch, width)
+        if isinstance(table, _tensor_type) and table.dtype is _I32 and table.get_device() == self.device and table.dim() == 2:
+            (batch, width), (row, col) = table.shape, table.stride()
+            if batch and width and (col == 1 or width == 1) and (row >= width or batch == 1):
+                return _KvTable(table.data_ptr(), row if batch > 1 else width, batch, width)
+            raise ValueError(f"{name} must be [batch, pages of a sequence] with unit stride along its rows, got {list(table.shape)}")
+        if not isinstance(table, _tensor_type) or table.dtype is not _I32:
+            raise TypeError(f"{name} must be an int32 torch tensor")
+        raise ValueError(f"{name} must be [batch, pages of a sequence] on cuda:{self.device}, got {list(table.shape)} on {table.device}")
 
     def _mass(self, mass, name: str, batch: int):
-        _check_op(mass, name, ("float32",), self.device)
-        if mass.dim() != 3 or tuple(mass.shape[:2]) != (batch, self.heads) or mass.shape[2] < 1 or \
+        if not isinstance(mass, _tensor_type) or mass.dtype is not _F32:
+            raise TypeError(f"{name} must be a float32 torch tensor")
+        if mass.get_device() != self.device or mass.dim() != 3 or tuple(mass.shape[:2]) != (batch, self.heads) or mass.shape[2] < 1 or \
                 (mass.shape[2] > 1 and mass.stride(2) != 1):
             raise ValueError(f"{name} must be [{batch}, {self.heads}, tokens] with unit stride along the tokens")
         rows = mass.stride(1) if self.heads > 1 else mass.shape[2]
@@ -660,11 +660,10 @@ def stagq_kv_append(cache: KVCache, k, v, table, starts, n: int, stream=None) ->
     position starts[b] on (a negative start: nothing). k, v: [batch * n,
     heads * dim]; table int32 [batch, pages]; starts int32 [batch]."""
     t, dev = cache._table(table), cache.device
-    _, ks = _check_rows(k, "k", t.batch * n, cache._row, cache._types, dev)
-    _, vs = _check_rows(v, "v", t.batch * n, cache._row, cache._types, dev)
-    _check_flat(starts, "starts", (t.batch,), "int32", dev)
-    _check(lib().stagq_kv_append(cache._c, t, starts.data_ptr(), k.data_ptr(), ks, v.data_ptr(), vs, n,
-                                 _op_stream(stream, dev)), "stagq_kv_append")
+    rows = t.batch * n
+    ks, vs = _check_rows(k, "k", rows, cache._row, cache._types, dev), _check_rows(v, "v", rows, cache._row, cache._types, dev)
+    _check(lib().stagq_kv_append(cache._c, t, _check_flat(starts, "starts", (t.batch,), _I32, dev), k.data_ptr(), ks,
+                                 v.data_ptr(), vs, n, _op_stream(stream, dev)), "stagq_kv_append")
 
 
 def stagq_kv_read(cache: KVCache, table, lens, k, v, n: int, starts=None, stream=None) -> None:
@@ -672,23 +671,25 @@ def stagq_kv_read(cache: KVCache, table, lens, k, v, n: int, starts=None, stream
     starts: from 0) as rows of k and v [batch * n, heads * dim], in the
     cache's type or fp32; zeros from lens[b] on (no lens: no bound)."""
     t, dev = cache._table(table), cache.device
-    dtype, ks = _check_rows(k, "k", t.batch * n, cache._row, (cache.dtype, "float32"), dev)
-    _, vs = _check_rows(v, "v", t.batch * n, cache._row, (dtype,), dev)
-    if starts is not None:
-        _check_flat(starts, "starts", (t.batch,), "int32", dev)
-    if lens is not None:
-        _check_flat(lens, "lens", (t.batch,), "int32", dev)
-    _check(lib().stagq_kv_read(cache._c, t, None if starts is None else starts.data_ptr(),
-                               None if lens is None else lens.data_ptr(), k.data_ptr(), ks, v.data_ptr(), vs, n,
-                               STAGQ_Y_F32 if dtype == "float32" else 0, _op_stream(stream, dev)), "stagq_kv_read")
+    rows = t.batch * n
+    ks = _check_rows(k, "k", rows, cache._row, (cache.dtype, _F32), dev)
+    vs = _check_rows(v, "v", rows, cache._row, (k.dtype,), dev)
+    _check(lib().stagq_kv_read(cache._c, t, starts if starts is None else _check_flat(starts, "starts", (t.batch,), _I32, dev),
+                               lens if lens is None else _check_flat(lens, "lens", (t.batch,), _I32, dev), k.data_ptr(), ks,
+                               v.data_ptr(), vs, n, STAGQ_Y_F32 if k.dtype is _F32 else 0, _op_stream(stream, dev)),
+           "stagq_kv_read")
 
 
 def stagq_kv_attention_workspace(cache: KVCache, batch: int, max_len: int, q_heads: int, n_new: int = 1,
                                  tracked: bool = False) -> int:
     """Workspace bytes of a stagq_kv_attention call (`tracked`: with a mass)."""
-    n = int(lib().stagq_kv_attention_workspace(cache._c, batch, max_len, q_heads, n_new, int(tracked)))
-    if n < 0:
-        raise ValueError(f"stagq_kv_attention_workspace: {lib().stagq_last_error().decode()}")
+    key = (batch, max_len, q_heads, n_new, bool(tracked))
+    n = cache._workspace.get(key)
+    if n is None:
+        n = int(lib().stagq_kv_attention_workspace(cache._c, batch, max_len, q_heads, n_new, int(tracked)))
+        if n < 0:
+            raise ValueError(f"stagq_kv_attention_workspace: {lib().stagq_last_error().decode()}")
+        cache._workspace[key] = n
     return n
 
 
@@ -703,14 +704,14 @@ def stagq_kv_attention(cache: KVCache, q, table, lens, out, n_new: int = 1, scal
     t = cache._table(table)
     dev = cache.device
     rows = t.batch * n_new
-    _check_op(q, "q", cache._types, dev)
+    if not isinstance(q, _tensor_type):
+        raise TypeError("q must be a torch tensor")
     cols = q.shape[-1]
     q_heads = cols // cache.dim
     if cols == 0 or cols % cache.dim:
         raise ValueError(f"q must be [{rows}, q_heads * {cache.dim}], got {list(q.shape)}")
-    _, qs = _check_rows(q, "q", rows, cols, cache._types, dev)
-    _, outs = _check_rows(out, "out", rows, cols, cache._types, dev)
-    _check_flat(lens, "lens", (t.batch,), "int32", dev)
+    qs, outs = _check_rows(q, "q", rows, cols, cache._types, dev), _check_rows(out, "out", rows, cols, cache._types, dev)
+    at_lens = _check_flat(lens, "lens", (t.batch,), _I32, dev)
     mb = mh = 0
     cap = t.width * cache.page
     if mass is not None:
@@ -723,15 +724,16 @@ def stagq_kv_attention(cache: KVCache, q, table, lens, out, n_new: int = 1, scal
     s = _op_stream(stream, dev)
     need = stagq_kv_attention_workspace(cache, t.batch, max_len, q_heads, n_new, mass is not None)
     if workspace is not None:
-        _check_op(workspace, "workspace", ("uint8",), dev)
-        if not workspace.is_contiguous():
-            raise ValueError("workspace must be contiguous")
+        if not isinstance(workspace, _tensor_type) or workspace.dtype is not _U8:
+            raise TypeError("workspace must be a uint8 torch tensor")
+        if workspace.get_device() != dev or not workspace.is_contiguous():
+            raise ValueError(f"workspace must be contiguous and on cuda:{dev}")
     elif need:
         import torch
         workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
         if stream is not None:  # the allocator must not reuse it while `stream` still does
             workspace.record_stream(torch.cuda.ExternalStream(s, device=dev))
-    _check(lib().stagq_kv_attention(cache._c, t, lens.data_ptr(), max_len, q.data_ptr(), qs, q_heads, n_new,
+    _check(lib().stagq_kv_attention(cache._c, t, at_lens, max_len, q.data_ptr(), qs, q_heads, n_new,
                                     cache.dim ** -0.5 if scale is None else scale, out.data_ptr(), outs,
                                     None if mass is None else mass.data_ptr(), mb, mh,
                                     None if workspace is None else workspace.data_ptr(),
@@ -748,19 +750,19 @@ def stagq_kv_evict(cache: KVCache, table, lens, mass, fresh, budget: int, recent
     dev = cache.device
     if f.batch != t.batch:
         raise ValueError("the two tables differ in batch")
-    _check_flat(lens, "lens", (t.batch,), "int32", dev)
+    at_lens = _check_flat(lens, "lens", (t.batch,), _I32, dev)
     mb, mh = cache._mass(mass, "mass", t.batch)
     nb, nh = cache._mass(new_mass, "new_mass", t.batch)
-    _check_flat(kept, "kept", (t.batch, cache.heads, budget), "int32", dev)
-    _check_flat(new_lens, "new_lens", (t.batch,), "int32", dev)
+    at_kept = _check_flat(kept, "kept", (t.batch, cache.heads, budget), _I32, dev)
+    at_new = _check_flat(new_lens, "new_lens", (t.batch,), _I32, dev)
     cap = min(t.width * cache.page, mass.shape[2])
     if max_len is None:
         max_len = cap
     elif max_len > cap:
         raise ValueError(f"max_len {max_len} exceeds the {cap} tokens of the table and the mass")
-    _check(lib().stagq_kv_evict(cache._c, t, lens.data_ptr(), max_len, mass.data_ptr(), mb, mh, budget, recent, f,
-                                kept.data_ptr(), new_lens.data_ptr(), new_mass.data_ptr(), nb, nh, new_mass.shape[2],
-                                _op_stream(stream, dev)), "stagq_kv_evict")
+    _check(lib().stagq_kv_evict(cache._c, t, at_lens, max_len, mass.data_ptr(), mb, mh, budget, recent, f, at_kept, at_new,
+                                new_mass.data_ptr(), nb, nh, new_mass.shape[2], _op_stream(stream, dev)),
+           "stagq_kv_evict")
 
 
 def stagq_ops_check(device: int = 0) -> None:

@@ -43,56 +43,63 @@ using kernels::smem_addr;
 
 constexpr int kQuantThreads = 256;
 
+// The 8-bit values of eight elements by the 64-bit quotient.
+__device__ __noinline__ uint2 quantize_exact(uint4 v, float amax, bool bf16) {
+  uint32_t w[2] = {0u, 0u};
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const uint32_t pair = i < 2 ? v.x : i < 4 ? v.y : i < 6 ? v.z : v.w;
+    const double f = ops::load16(static_cast<uint16_t>(pair >> (16 * (i & 1))), bf16);
+    w[i >> 2] |= (static_cast<uint32_t>(static_cast<int>(rint(f * 127.0 / static_cast<double>(amax)))) & 255u) << (8 * (i & 3));
+  }
+  return make_uint2(w[0], w[1]);
+}
+
 // One row per CTA, held in registers between its maximum and its rounding, so
-// x is read once: 2 bytes in and 1 out per element, bound by bytes. The
-// quotient that decides q is the binary64 one; fp32 agrees with it unless it
-// is within 1e-3 of a half (its error is below 127 * 3 * 2^-24 = 2.3e-5), and
-// only those elements divide in 64 bits.
-template <int STEPS>
+// x is read once: 2 bytes in and 1 out per element, bound by bytes. Two
+// elements at a time share the maximum of their magnitudes' bits. q comes from
+// an approximate reciprocal and is checked by the remainder 127 x - q a, which
+// fp32 has exactly (18 bits against 18): no division, and ties are settled by
+// it too. Rows whose a is out of fp32's reach for that divide in 64 bits.
+template <int STEPS, bool BF>
 __global__ void __launch_bounds__(kQuantThreads) quantize_i8_kernel(const __grid_constant__ QuantizeI8Args a) {
-  __shared__ float s_max[kQuantThreads / 32];
-  __shared__ int s_bad[kQuantThreads / 32];
+  __shared__ uint32_t s_top[kQuantThreads / 32];
   grid_launch_dependents();
   grid_dependency_wait();
   const int row = blockIdx.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const uint16_t* x = a.x + static_cast<int64_t>(row) * a.x_stride;
-  uint16_t v[STEPS][8];
+  uint32_t v[STEPS][4];
+  uint32_t top = 0;  // bits of the largest magnitude, in either half
 #pragma unroll
   for (int s = 0; s < STEPS; ++s) {
     const int c = (s * kQuantThreads + threadIdx.x) * 8;
-    if (c + 8 <= a.in) {
-      ops::load8(x + c, a.vec, v[s]);
+    if (a.vec && c + 8 <= a.in) {
+      const uint4 w = *reinterpret_cast<const uint4*>(x + c);
+      v[s][0] = w.x;
+      v[s][1] = w.y;
+      v[s][2] = w.z;
+      v[s][3] = w.w;
     } else {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) v[s][i] = c + i < a.in ? x[c + i] : static_cast<uint16_t>(0);
+      for (int i = 0; i < 4; ++i)
+        v[s][i] = ops::pack2(c + 2 * i < a.in ? x[c + 2 * i] : static_cast<uint16_t>(0),
+                             c + 2 * i + 1 < a.in ? x[c + 2 * i + 1] : static_cast<uint16_t>(0));
     }
   }
-  float amax = 0.0f;
-  bool fine = true;
 #pragma unroll
   for (int s = 0; s < STEPS; ++s)
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const float f = ops::load16(v[s][i], a.bf16);
-      fine = fine && isfinite(f);
-      amax = fmaxf(amax, fabsf(f));
-    }
-#pragma unroll
-  for (int d = 1; d < 32; d <<= 1) amax = fmaxf(amax, __shfl_xor_sync(kFull, amax, d));
-  const bool bad = __any_sync(kFull, !fine);
-  if (lane == 0) {
-    s_max[warp] = amax;
-    s_bad[warp] = bad;
-  }
+    for (int i = 0; i < 4; ++i) top = __vmaxu2(top, v[s][i] & 0x7FFF7FFFu);
+  top = max(top & 0xFFFFu, top >> 16);
+  top = __reduce_max_sync(kFull, top);
+  if (lane == 0) s_top[warp] = top;
   __syncthreads();
-  int any_bad = 0;
 #pragma unroll
-  for (int w = 0; w < kQuantThreads / 32; ++w) {
-    amax = fmaxf(amax, s_max[w]);
-    any_bad |= s_bad[w];
-  }
-  if (threadIdx.x == 0) a.scale[row] = any_bad ? __uint_as_float(0x7FC00000u) : amax / 127.0f;
-  const bool zero = any_bad || amax == 0.0f;
+  for (int w = 0; w < kQuantThreads / 32; ++w) top = max(top, s_top[w]);
+  const bool bad = top >= (BF ? 0x7F80u : 0x7C00u);
+  const float amax = ops::load16(static_cast<uint16_t>(top), BF);
+  if (threadIdx.x == 0) a.scale[row] = bad ? __uint_as_float(0x7FC00000u) : amax / 127.0f;
+  const bool zero = bad || top == 0;
   const float inv = 127.0f / amax;
   int8_t* q = a.q + static_cast<int64_t>(row) * a.ld;
 #pragma unroll
@@ -101,13 +108,34 @@ __global__ void __launch_bounds__(kQuantThreads) quantize_i8_kernel(const __grid
     if (c >= a.ld) break;
     uint32_t w[2] = {0u, 0u};
     if (!zero) {
+      constexpr float kRound = 12582912.0f;  // 1.5 * 2^23: a sum with it is rounded to a whole number
+      if (amax > 1e-30f && amax < 1e36f) {
+        uint32_t bits[8];
+        float far = 0.0f;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const float f = ops::load16(v[s][i], a.bf16);
-        const float p = f * inv;
-        float r = rintf(p);
-        if (!(fabsf(p - r) <= 0.499f)) r = static_cast<float>(rint(static_cast<double>(f) * 127.0 / static_cast<double>(amax)));
-        w[i >> 2] |= (static_cast<uint32_t>(static_cast<int>(r)) & 255u) << (8 * (i & 3));
+        for (int i = 0; i < 8; ++i) {
+          const float f = ops::load16(static_cast<uint16_t>(v[s][i >> 1] >> (16 * (i & 1))), BF);
+          const float r = fmaf(f, inv, kRound);
+          bits[i] = __float_as_uint(r);  // its lowest byte is q
+          far = fmaxf(far, fabsf(fmaf(kRound - r, amax, 127.0f * f)));
+        }
+        if (far * 2.0f >= amax) {  // a tie, or one off next to a half
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const float f = ops::load16(static_cast<uint16_t>(v[s][i >> 1] >> (16 * (i & 1))), BF);
+            const float rest = 2.0f * fmaf(kRound - __uint_as_float(bits[i]), amax, 127.0f * f);
+            const bool odd = bits[i] & 1u;
+            bits[i] += (rest > amax || (rest == amax && odd)) - (rest < -amax || (rest == -amax && odd));
+          }
+        }
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+          w[i] = __byte_perm(__byte_perm(bits[4 * i], bits[4 * i + 1], 0x0040),
+                             __byte_perm(bits[4 * i + 2], bits[4 * i + 3], 0x0040), 0x5410);
+      } else {
+        const uint2 exact = quantize_exact(make_uint4(v[s][0], v[s][1], v[s][2], v[s][3]), amax, BF);
+        w[0] = exact.x;
+        w[1] = exact.y;
       }
     }
     *reinterpret_cast<uint2*>(q + c) = make_uint2(w[0], w[1]);
@@ -441,13 +469,22 @@ GemmI8Plan plan_gemm_i8(int n, int out, int kblocks, int num_sms) {
   return p;
 }
 
+namespace {
+
+template <bool BF>
+cudaError_t launch_quantize(const QuantizeI8Args& a, int steps, cudaStream_t s) {
+  const dim3 grid(a.n), block(kQuantThreads);
+  if (steps <= 2) return launch_op(quantize_i8_kernel<2, BF>, grid, block, 0, s, a);
+  if (steps <= 4) return launch_op(quantize_i8_kernel<4, BF>, grid, block, 0, s, a);
+  if (steps <= 8) return launch_op(quantize_i8_kernel<8, BF>, grid, block, 0, s, a);
+  return launch_op(quantize_i8_kernel<16, BF>, grid, block, 0, s, a);
+}
+
+}  // namespace
+
 cudaError_t launch_quantize_i8(const QuantizeI8Args& a, cudaStream_t s) {
   const int steps = (a.ld + kQuantThreads * 8 - 1) / (kQuantThreads * 8);
-  const dim3 grid(a.n), block(kQuantThreads);
-  if (steps <= 2) return launch_op(quantize_i8_kernel<2>, grid, block, 0, s, a);
-  if (steps <= 4) return launch_op(quantize_i8_kernel<4>, grid, block, 0, s, a);
-  if (steps <= 8) return launch_op(quantize_i8_kernel<8>, grid, block, 0, s, a);
-  return launch_op(quantize_i8_kernel<16>, grid, block, 0, s, a);
+  return a.bf16 ? launch_quantize<true>(a, steps, s) : launch_quantize<false>(a, steps, s);
 }
 
 cudaError_t launch_gemm_i8(GemmI8Args a, const GemmI8Plan& p, const int8_t* xq, const int8_t* wq, int ld,

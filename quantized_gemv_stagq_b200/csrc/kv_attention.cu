@@ -274,6 +274,7 @@ __global__ void __launch_bounds__(kWarps * 32, resident_ctas(NT, NG)) kv_attenti
         if (lane >= d) sum += o;
       }
       const uint32_t past = __ballot_sync(kFull, before + sum > at);
+      if (b0 >= a.batch) return;
       if (past) {
         const int l = __ffs(past) - 1;
         b = b0 + l;
@@ -290,9 +291,11 @@ __global__ void __launch_bounds__(kWarps * 32, resident_ctas(NT, NG)) kv_attenti
     rounds = rounds_of(a, b);
     while (at >= before + rounds * units_b) {
       before += rounds * units_b;
-      rounds = rounds_of(a, ++b);
+      if (++b >= a.batch) return;  // here and below: lengths that changed under the call write nothing out of bounds
+      rounds = rounds_of(a, b);
     }
     unit = (at - before) / rounds;  // of the sequence
+    if (unit >= units_b) return;
     round0 = at - before - unit * rounds;
     n_rounds = min(rounds - round0, run_end - at);
     if (round0 == 0 && threadIdx.x == 0 && a.part_o)  // where the join finds the unit's partial sums
@@ -801,7 +804,7 @@ __global__ void __launch_bounds__(512) kv_join_kernel(const __grid_constant__ Kv
     const int h = unit / a.row_blocks, r = (unit - h * a.row_blocks) * ROWS + row;
     if (r >= a.rows || a.lens[b] <= 0) return;
     const int4 p = a.parts[u];
-    if (p.x == p.y) return;  // one CTA wrote the unit out
+    if (p.x == p.y || p.x < 0 || p.x > p.y || p.y >= a.ctas) return;  // one CTA wrote the unit out
     const int group = threadIdx.x / D, d = threadIdx.x - group * D;
     float top = -INFINITY, den = 0.0f, sum = 0.0f;
     for (int c0 = p.x + group; c0 <= p.y; c0 += 4 * GROUPS) {
@@ -871,7 +874,8 @@ __global__ void __launch_bounds__(512) kv_join_kernel(const __grid_constant__ Kv
   const int lane = threadIdx.x & 31;
   for (int r = threadIdx.x >> 5; r < a.rows; r += 16) {
     const int rb = r / ROWS, row = r - rb * ROWS;
-    const int4 p = a.parts[b * units_b + h * a.row_blocks + rb];
+    int4 p = a.parts[b * units_b + h * a.row_blocks + rb];
+    if (p.x < 0 || p.x > p.y || p.y >= a.ctas) p.x = p.y;  // not a record: the lengths changed under the call
     float top, den;
     if (p.x == p.y) {
       const float2 ml = a.unit_ml[static_cast<int64_t>(bh) * a.rows_pad + r];

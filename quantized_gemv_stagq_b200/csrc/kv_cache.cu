@@ -34,150 +34,252 @@ __device__ __forceinline__ uint8_t* kv_block(const KvView& kv, int64_t b, int64_
   return kv.pages + static_cast<int64_t>(pid) * kv.page_stride + static_cast<int64_t>(2 * head + which) * kv.block_bytes;
 }
 
+// Append and read: dim / 8 lanes take a token's K and V rows of one head, 8
+// consecutive channels each, so that a row's code bytes move in one coalesced
+// access. Items are numbered (token, head, lane) and found again by
+// multiplications (Divider): the kernels are bound by bytes only as long as
+// finding an item costs less than moving it, which is also why an item is K
+// and V (one page lookup for both).
+struct Item {
+  int tok, head, c8;  // token row of the call; c8: channels 8 c8 .. 8 c8 + 7
+};
+__device__ __forceinline__ Item item_of(const KvRowsArgs& a, int tok0, uint32_t i) {
+  const uint32_t t = a.per_token.divide(i), rest = i - t * a.per_token.d;
+  const int shift = a.kv.dim == 128 ? 4 : 3;  // lanes per row
+  return {tok0 + static_cast<int>(t), static_cast<int>(rest >> shift), static_cast<int>(rest) & ((1 << shift) - 1)};
+}
+
+constexpr int kRowThreads = 256;
+constexpr float kWhole = 12582912.0f;  // 1.5 * 2^23: a sum with it is rounded to a whole number
+
 // ------------------------------------------------------------------ append
 
-// Bound by bytes: 4 per channel read (K and V), about 1 written. dim / 8 lanes
-// take a row (one token, head, K or V), 8 consecutive channels each, so that a
-// row's code bytes leave in one coalesced store.
-__global__ void __launch_bounds__(256) kv_append_kernel(const __grid_constant__ KvRowsArgs a) {
+// The rounding error of d = x - y in fp32 (Moller and Knuth's two-sum): 0 if d is exact.
+__device__ __forceinline__ float difference_error(float x, float y, float d) {
+  const float z = d - x;
+  return (x - (d - z)) - (y + z);
+}
+
+// RN16((hi - lo) / 15). fp32 gives it unless it lies within 8 ulp of a tie
+// between two 16-bit values (its error is below 4); there the remainder's sign,
+// which one multiply-add has exactly, decides. Where hi - lo is not exact or
+// fp32's own spacing widens, 64 bits do.
+template <bool BF>
+__device__ __forceinline__ uint16_t scale16(float lo, float hi) {
+  const float d = hi - lo, s = d * (1.0f / 15.0f);
+  const uint32_t bits = __float_as_uint(s), tie = BF ? 0x8000u : 0x1000u;
+  const int cut = static_cast<int>(bits & (2 * tie - 1)) - static_cast<int>(tie);
+  if (s > (BF ? 1e-36f : 6.2e-5f) && s < 1e37f) {
+    if (cut > 8 || cut < -8) return ops::store16(s, BF);
+    if (difference_error(hi, lo, d) == 0.0f) {
+      const uint32_t middle = (bits & ~(2 * tie - 1)) | tie;
+      const float rest = fmaf(-15.0f, __uint_as_float(middle), d);
+      return ops::store16(__uint_as_float(rest > 0.0f ? middle + 1 : rest < 0.0f ? middle - 1 : middle), BF);
+    }
+  }
+  return ops::store16_from_double((static_cast<double>(hi) - static_cast<double>(lo)) / 15.0, BF);
+}
+
+// The codes of eight channels by the 64-bit quotient.
+__device__ __noinline__ uint32_t exact_codes(uint4 v, float lo, float s, bool bf16) {
+  uint32_t word = 0;
+  for (int k = 0; k < 8; ++k) {
+    const uint32_t pair = k < 2 ? v.x : k < 4 ? v.y : k < 6 ? v.z : v.w;
+    const double x = ops::load16(static_cast<uint16_t>(pair >> (16 * (k & 1))), bf16);
+    const double u = rint((x - static_cast<double>(lo)) / static_cast<double>(s));
+    word |= static_cast<uint32_t>(fmin(u, 15.0)) << (4 * k);
+  }
+  return word;
+}
+
+template <bool BF>
+__device__ __forceinline__ uint32_t min2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  if (BF)
+    asm("min.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  else
+    asm("min.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+template <bool BF>
+__device__ __forceinline__ uint32_t max2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  if (BF)
+    asm("max.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  else
+    asm("max.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+
+__device__ __forceinline__ uint4 load8_packed(const uint16_t* p, bool vec) {
+  if (vec) return *reinterpret_cast<const uint4*>(p);
+  return make_uint4(ops::pack2(p[0], p[1]), ops::pack2(p[2], p[3]), ops::pack2(p[4], p[5]), ops::pack2(p[6], p[7]));
+}
+
+// Codes (nibble k: channel k of the lane's eight) and the group's pair. All
+// lanes of the warp take part; a group is `glanes` neighbouring ones.
+template <bool BF>
+__device__ __forceinline__ uint32_t round8(const uint4& v, int glanes, uint32_t& pair) {
+  uint32_t lo2 = min2<BF>(min2<BF>(v.x, v.y), min2<BF>(v.z, v.w));
+  uint32_t hi2 = max2<BF>(max2<BF>(v.x, v.y), max2<BF>(v.z, v.w));
+  uint32_t top = __vmaxu2(__vmaxu2(v.x & 0x7FFF7FFFu, v.y & 0x7FFF7FFFu), __vmaxu2(v.z & 0x7FFF7FFFu, v.w & 0x7FFF7FFFu));
+  for (int d = 1; d < glanes; d <<= 1) {
+    lo2 = min2<BF>(lo2, __shfl_xor_sync(kFull, lo2, d));
+    hi2 = max2<BF>(hi2, __shfl_xor_sync(kFull, hi2, d));
+    top = __vmaxu2(top, __shfl_xor_sync(kFull, top, d));
+  }
+  const bool fine = max(top & 0xFFFFu, top >> 16) < (BF ? 0x7F80u : 0x7C00u);
+  if (!fine) {
+    pair = BF ? 0x7FC07FC0u : 0x7E007E00u;
+    return 0u;
+  }
+  const float lo = fminf(ops::load16(static_cast<uint16_t>(lo2), BF), ops::load16(static_cast<uint16_t>(lo2 >> 16), BF));
+  const float hi = fmaxf(ops::load16(static_cast<uint16_t>(hi2), BF), ops::load16(static_cast<uint16_t>(hi2 >> 16), BF));
+  const uint16_t s16 = scale16<BF>(lo, hi);
+  const float s = ops::load16(s16, BF);
+  pair = ops::pack2(s16, ops::store16(lo, BF));  // exact: lo is one of the inputs
+  if (s == 0.0f) return 0u;
+  const float inv = __frcp_rn(s);
+  if (s < (BF ? 1e-36f : 6.2e-5f) || !(hi - lo < 1e37f)) return exact_codes(v, lo, s, BF);
+  // The quotient of d = x - lo and s, correctly rounded by Markstein's method (a
+  // correctly rounded reciprocal, one correction), so that ties, which are
+  // common where K and V have few bits, are exact halves and round to even. It
+  // is checked by the remainder d - u s, which a multiply-add has exactly if d
+  // is exact: more than s / 2 means a quotient next to a half that rounded to
+  // it. d is exact if no element lies more than 2^16 (fp16: 2^13) below the
+  // group's largest, 24 bits spanning them; if not, a remainder near s / 2
+  // decides nothing. Either leaves the lane's eight to 64 bits.
+  uint32_t word = 0;
+  float far = 0.0f;
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+  for (int k = 7; k >= 0; --k) {
+    const float d = ops::load16(static_cast<uint16_t>(w[k >> 1] >> (16 * (k & 1))), BF) - lo;
+    const float q0 = d * inv;
+    const float r = fmaf(fmaf(-q0, s, d), inv, q0) + kWhole;
+    far = fmaxf(far, fabsf(fmaf(kWhole - r, s, d)));
+    word = word * 16u + __float_as_uint(r);  // the lowest 4 bits of r are the code
+  }
+  word -= 0x4B400000u * 0x11111111u;
+  if (far >= s * 0.49999f) {
+    uint32_t low = 0xFFFFFFFFu;  // the smallest magnitudes' bits less 1 (zero: the largest)
+#pragma unroll
+    for (int k = 0; k < 4; ++k) low = __vminu2(low, __vsub2(w[k] & 0x7FFF7FFFu, 0x00010001u));
+    const int smallest = min(min(low & 0xFFFFu, low >> 16), static_cast<uint32_t>(ops::store16(fabsf(lo), BF) - 1) & 0xFFFFu);
+    const int largest = static_cast<int>(max(top & 0xFFFFu, top >> 16));
+    if (far > s * 0.5f || smallest < largest - (BF ? 16 * 128 : 13 * 1024)) word = exact_codes(v, lo, s, BF);
+  }
+  return word;
+}
+
+// Bound by bytes: 4 per channel read (K and V), about 1 written.
+template <bool BF>
+__global__ void __launch_bounds__(kRowThreads) kv_append_kernel(const __grid_constant__ KvRowsArgs a) {
   grid_launch_dependents();
   grid_dependency_wait();
   const KvView& kv = a.kv;
-  const int lanes = kv.dim >> 3;                       // 8 or 16 lanes per row
-  const int64_t row = (blockIdx.x * static_cast<int64_t>(blockDim.x) + threadIdx.x) / lanes;
-  const int c8 = threadIdx.x & (lanes - 1);            // its channels: 8 c8 .. 8 c8 + 7
-  const int64_t unit = row >> 1;                       // (token row, head)
-  const int which = static_cast<int>(row & 1);
-  const bool in = unit < a.n_rows * kv.heads;
-  const int64_t tok = in ? unit / kv.heads : 0;
-  const int head = in ? static_cast<int>(unit - tok * kv.heads) : 0;
-  const int64_t b = tok / a.n;
-  const int start = a.starts[b];
-  const int64_t pos = start < 0 ? -1 : start + (tok - b * a.n);
-  uint8_t* block = kv_block(kv, b, pos, head, which);
-  if (in && !block && start >= 0 && c8 == 0) atomicOr(&g_status, kOpsBadPage);
-  const bool live = in && block;
-
-  uint16_t raw[8];
-  const uint16_t* src = static_cast<const uint16_t*>(which ? a.v : a.k) + tok * (which ? a.v_stride : a.k_stride) +
-                        head * kv.dim + 8 * c8;
-  if (live) {
-    ops::load8(src, a.vec, raw);
-  } else {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) raw[i] = 0;
-  }
-  float x[8], lo, hi;
-  bool fine = true;
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    x[i] = ops::load16(raw[i], kv.bf16);
-    fine = fine && isfinite(x[i]);
-    lo = i ? fminf(lo, x[i]) : x[0];
-    hi = i ? fmaxf(hi, x[i]) : x[0];
-  }
+  const int tok0 = blockIdx.x * a.cta_tokens;
+  const uint32_t n_items = min(a.cta_tokens, static_cast<int>(a.n_rows) - tok0) * a.per_token.d;
   const int glanes = kv.group >> 3;
-  for (int d = 1; d < glanes; d <<= 1) {
-    lo = fminf(lo, __shfl_xor_sync(kFull, lo, d));
-    hi = fmaxf(hi, __shfl_xor_sync(kFull, hi, d));
-    fine = __shfl_xor_sync(kFull, fine ? 1 : 0, d) && fine;
-  }
-  if (!live) return;
-
-  const uint16_t s16 = ops::store16_from_double((static_cast<double>(hi) - static_cast<double>(lo)) / 15.0, kv.bf16);
-  const float s = ops::load16(s16, kv.bf16);
-  const float inv = 1.0f / s;
-  uint32_t word = 0;
-  if (fine && s > 0.0f) {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const float t = (x[i] - lo) * inv;
-      float u = rintf(t);
-      // t is within 16 * 3 * 2^-24 of the quotient; also taken when t is not finite
-      if (!(fabsf(t - u) <= 0.4999f))
-        u = static_cast<float>(rint((static_cast<double>(x[i]) - static_cast<double>(lo)) / static_cast<double>(s)));
-      word |= static_cast<uint32_t>(fminf(u, 15.0f)) << (4 * i);
+  for (uint32_t i0 = 0; i0 < n_items; i0 += kRowThreads) {
+    const uint32_t i = i0 + threadIdx.x;
+    const bool in = i < n_items;
+    const Item it = item_of(a, tok0, in ? i : 0);
+    const int c = it.head * kv.dim + 8 * it.c8;
+    const uint4 k = load8_packed(static_cast<const uint16_t*>(a.k) + it.tok * a.k_stride + c, a.vec);
+    const uint4 v = load8_packed(static_cast<const uint16_t*>(a.v) + it.tok * a.v_stride + c, a.vec);
+    const int b = static_cast<int>(a.per_sequence.divide(it.tok));
+    const int start = a.starts[b];
+    const int64_t pos = start < 0 ? -1 : static_cast<int64_t>(start) + (it.tok - b * a.n);
+    uint8_t* block = kv_block(kv, b, pos, it.head, 0);
+    if (in && !block && start >= 0 && it.c8 == 0) atomicOr(&g_status, kOpsBadPage);
+    uint32_t pair_k, pair_v;
+    const uint32_t word_k = round8<BF>(k, glanes, pair_k), word_v = round8<BF>(v, glanes, pair_v);
+    // V: the lane of blocks j and j ^ 1 swap halves, so that each has 4 bytes in a row
+    const int j = it.c8 >> 2, t = it.c8 & 3;
+    const uint32_t other = __shfl_xor_sync(kFull, word_v, 4);
+    const uint32_t bytes_v = j & 1 ? __byte_perm(other, word_v, 0x7632) : __byte_perm(word_v, other, 0x5410);
+    if (!in || !block) continue;
+    const int slot = static_cast<int>(pos & (kv.page - 1)), half = kv.dim >> 1;
+    uint8_t* at = block + slot * half;
+    *reinterpret_cast<uint32_t*>(at + t * (kv.dim >> 3) + 4 * j) = word_k;
+    at += kv.block_bytes;
+    *reinterpret_cast<uint32_t*>(at + (2 * t + (j & 1)) * (kv.dim >> 4) + 2 * (j & ~1)) = bytes_v;
+    if ((it.c8 & (glanes - 1)) == 0) {
+      uint8_t* meta = block + kv.page * half + 4 * (slot * a.groups + (it.c8 >> a.group_shift));
+      *reinterpret_cast<uint32_t*>(meta) = pair_k;
+      *reinterpret_cast<uint32_t*>(meta + kv.block_bytes) = pair_v;
     }
-  }
-  const int slot = static_cast<int>(pos & (kv.page - 1));
-  uint8_t* codes = block + slot * (kv.dim >> 1);
-  const int j = c8 >> 2, t = c8 & 3;
-  if (which == 0) {
-    *reinterpret_cast<uint32_t*>(codes + t * (kv.dim >> 3) + 4 * j) = word;
-  } else {
-    *reinterpret_cast<uint16_t*>(codes + (2 * t) * (kv.dim >> 4) + 2 * j) = static_cast<uint16_t>(word);
-    *reinterpret_cast<uint16_t*>(codes + (2 * t + 1) * (kv.dim >> 4) + 2 * j) = static_cast<uint16_t>(word >> 16);
-  }
-  if ((c8 & (glanes - 1)) == 0) {
-    const uint16_t nan = kv.bf16 ? 0x7FC0 : 0x7E00;
-    const uint16_t lo16 = ops::store16(lo, kv.bf16);   // exact: lo is one of the inputs
-    uint32_t* meta = reinterpret_cast<uint32_t*>(block + kv.page * (kv.dim >> 1)) + slot * (kv.dim / kv.group);
-    meta[8 * c8 / kv.group] = fine ? ops::pack2(s16, lo16) : ops::pack2(nan, nan);
   }
 }
 
 // -------------------------------------------------------------------- read
 
-// The values of positions starts[b] + i, i < n; rows at or past lens[b], and
-// rows whose page is bad, are zero. Lanes as in kv_append_kernel.
-__global__ void __launch_bounds__(256) kv_read_kernel(const __grid_constant__ KvRowsArgs a) {
-  grid_launch_dependents();
-  grid_dependency_wait();
-  const KvView& kv = a.kv;
-  const int lanes = kv.dim >> 3;
-  const int64_t row = (blockIdx.x * static_cast<int64_t>(blockDim.x) + threadIdx.x) / lanes;
-  const int c8 = threadIdx.x & (lanes - 1);
-  const int64_t unit = row >> 1;
-  const int which = static_cast<int>(row & 1);
-  if (unit >= a.n_rows * kv.heads) return;
-  const int64_t tok = unit / kv.heads;
-  const int head = static_cast<int>(unit - tok * kv.heads);
-  const int64_t b = tok / a.n;
-  const int64_t pos = (a.starts ? a.starts[b] : 0) + (tok - b * a.n);
-  float x[8] = {};
-  const bool inside = pos >= 0 && (!a.lens || pos < a.lens[b]);
-  uint8_t* block = inside ? kv_block(kv, b, pos, head, which) : nullptr;
-  if (inside && !block && c8 == 0) atomicOr(&g_status, kOpsBadPage);
-  if (block) {
-    const int slot = static_cast<int>(pos & (kv.page - 1));
-    const uint8_t* codes = block + slot * (kv.dim >> 1);
-    const int j = c8 >> 2, t = c8 & 3;
-    uint32_t word;
-    if (which == 0) {
-      word = *reinterpret_cast<const uint32_t*>(codes + t * (kv.dim >> 3) + 4 * j);
-    } else {
-      word = ops::pack2(*reinterpret_cast<const uint16_t*>(codes + (2 * t) * (kv.dim >> 4) + 2 * j),
-                        *reinterpret_cast<const uint16_t*>(codes + (2 * t + 1) * (kv.dim >> 4) + 2 * j));
-    }
-    const uint32_t m = (reinterpret_cast<const uint32_t*>(block + kv.page * (kv.dim >> 1)) +
-                        slot * (kv.dim / kv.group))[8 * c8 / kv.group];
-    const float s = ops::load16(static_cast<uint16_t>(m), kv.bf16), lo = ops::load16(static_cast<uint16_t>(m >> 16), kv.bf16);
+template <bool BF, bool F32>
+__device__ __forceinline__ void write8(void* base, int64_t at, uint32_t word, uint32_t pair, bool vec) {
+  const float s = ops::load16(static_cast<uint16_t>(pair), BF), lo = ops::load16(static_cast<uint16_t>(pair >> 16), BF);
+  float x[8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) x[i] = fmaf(s, static_cast<float>((word >> (4 * i)) & 15u), lo);
-  }
-  const int64_t at = tok * (which ? a.v_stride : a.k_stride) + head * kv.dim + 8 * c8;
-  void* base = which ? a.v : a.k;
-  if (a.f32) {
+  for (int k = 0; k < 8; ++k)  // a code under the exponent of 2^23 is 2^23 + u
+    x[k] = fmaf(s, __uint_as_float(((word >> (4 * k)) & 15u) | 0x4B000000u) - 8388608.0f, lo);
+  if (F32) {
     float* dst = static_cast<float*>(base) + at;
-    if (a.vec) {
+    if (vec) {
       reinterpret_cast<float4*>(dst)[0] = make_float4(x[0], x[1], x[2], x[3]);
       reinterpret_cast<float4*>(dst)[1] = make_float4(x[4], x[5], x[6], x[7]);
     } else {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) dst[i] = x[i];
+      for (int k = 0; k < 8; ++k) dst[k] = x[k];
     }
   } else {
     uint16_t* dst = static_cast<uint16_t*>(base) + at;
     uint16_t y[8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) y[i] = ops::store16(x[i], kv.bf16);
-    if (a.vec) {
+    for (int k = 0; k < 8; ++k) y[k] = ops::store16(x[k], BF);
+    if (vec) {
       *reinterpret_cast<uint4*>(dst) =
           make_uint4(ops::pack2(y[0], y[1]), ops::pack2(y[2], y[3]), ops::pack2(y[4], y[5]), ops::pack2(y[6], y[7]));
     } else {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) dst[i] = y[i];
+      for (int k = 0; k < 8; ++k) dst[k] = y[k];
     }
+  }
+}
+
+// The values of positions starts[b] + i, i < n; rows at or past lens[b], and
+// rows whose page is bad, are zero (code 0, scale 0, lowest 0).
+template <bool BF, bool F32>
+__global__ void __launch_bounds__(kRowThreads) kv_read_kernel(const __grid_constant__ KvRowsArgs a) {
+  grid_launch_dependents();
+  grid_dependency_wait();
+  const KvView& kv = a.kv;
+  const int tok0 = blockIdx.x * a.cta_tokens;
+  const uint32_t n_items = min(a.cta_tokens, static_cast<int>(a.n_rows) - tok0) * a.per_token.d;
+  const int half = kv.dim >> 1;
+#pragma unroll 2
+  for (uint32_t i = threadIdx.x; i < n_items; i += kRowThreads) {
+    const Item it = item_of(a, tok0, i);
+    const int b = static_cast<int>(a.per_sequence.divide(it.tok));
+    const int64_t pos = static_cast<int64_t>(a.starts ? a.starts[b] : 0) + (it.tok - b * a.n);
+    const bool inside = pos >= 0 && (!a.lens || pos < a.lens[b]);
+    const uint8_t* block = inside ? kv_block(kv, b, pos, it.head, 0) : nullptr;
+    if (inside && !block && it.c8 == 0) atomicOr(&g_status, kOpsBadPage);
+    uint32_t word_k = 0, word_v = 0, pair_k = 0, pair_v = 0;
+    if (block) {
+      const int slot = static_cast<int>(pos & (kv.page - 1));
+      const int j = it.c8 >> 2, t = it.c8 & 3;
+      const uint8_t* at = block + slot * half;
+      word_k = *reinterpret_cast<const uint32_t*>(at + t * (kv.dim >> 3) + 4 * j);
+      at += kv.block_bytes;
+      word_v = ops::pack2(*reinterpret_cast<const uint16_t*>(at + (2 * t) * (kv.dim >> 4) + 2 * j),
+                          *reinterpret_cast<const uint16_t*>(at + (2 * t + 1) * (kv.dim >> 4) + 2 * j));
+      const uint8_t* meta = block + kv.page * half + 4 * (slot * a.groups + (it.c8 >> a.group_shift));
+      pair_k = *reinterpret_cast<const uint32_t*>(meta);
+      pair_v = *reinterpret_cast<const uint32_t*>(meta + kv.block_bytes);
+    }
+    const int c = it.head * kv.dim + 8 * it.c8;
+    write8<BF, F32>(a.k, it.tok * a.k_stride + c, word_k, pair_k, a.vec);
+    write8<BF, F32>(a.v, it.tok * a.v_stride + c, word_v, pair_v, a.vec);
   }
 }
 
@@ -198,11 +300,15 @@ __device__ __forceinline__ uint32_t mass_key(float m) {
 // in their order. A radix selection finds the want-th largest key 8 bits at a
 // time; every lane counts into its own copy of the histogram (256 x 32
 // counters), so equal keys, which a mass of mostly one exponent is full of, do
-// not queue on one shared-memory word. Two passes then number the kept tokens.
+// not queue on one shared-memory word. Then every 32 tokens count their kept
+// ones, a scan over the counts numbers them, and the kept positions are written.
+// Up to KEYS * 1024 tokens are read once and stay in registers; KEYS = 0 reads
+// them again in each of the six passes (they come from L2).
+template <int KEYS>
 __global__ void __launch_bounds__(kSelThreads) kv_select_kernel(const __grid_constant__ KvEvictArgs a) {
   __shared__ int hist[kBins][32];
   __shared__ int total[kBins];
-  __shared__ int n_above[kSelWarps], n_equal[kSelWarps];
+  __shared__ int2 sums[kSelWarps];
   __shared__ uint32_t s_prefix;
   __shared__ int s_want;
   grid_launch_dependents();
@@ -227,6 +333,25 @@ __global__ void __launch_bounds__(kSelThreads) kv_select_kernel(const __grid_con
   if (want == 0) return;
 
   const float* mass = a.mass + b * a.mass_stride_b + h * a.mass_stride_h;
+  constexpr int HELD = KEYS > 0 ? KEYS : 1;
+  uint32_t keys[HELD];
+  if (KEYS > 0) {
+#pragma unroll
+    for (int k = 0; k < HELD; ++k) {
+      const int i = k * kSelThreads + tid;
+      keys[k] = i < old ? mass_key(mass[i]) : 0u;
+    }
+  }
+  // f(token, key) for the thread's tokens: tid, tid + 1024, ...
+  auto each = [&](auto&& f) {
+    if (KEYS > 0) {
+#pragma unroll
+      for (int k = 0; k < HELD; ++k)
+        if (k * kSelThreads + tid < old) f(keys[k]);
+    } else {
+      for (int i = tid; i < old; i += kSelThreads) f(mass_key(mass[i]));
+    }
+  };
   if (tid == 0) {
     s_prefix = 0;
     s_want = want;
@@ -236,10 +361,9 @@ __global__ void __launch_bounds__(kSelThreads) kv_select_kernel(const __grid_con
     __syncthreads();
     const uint32_t prefix = s_prefix, mask = shift == 24 ? 0u : 0xFFFFFFFFu << (shift + 8);
     const int left = s_want;
-    for (int i = tid; i < old; i += kSelThreads) {
-      const uint32_t key = mass_key(mass[i]);
+    each([&](uint32_t key) {
       if (((key ^ prefix) & mask) == 0) atomicAdd(&hist[(key >> shift) & 255u][lane], 1);
-    }
+    });
     __syncthreads();
     for (int i = warp; i < kBins; i += kSelWarps) {
       const int n = __reduce_add_sync(kFull, hist[i][lane]);
@@ -266,99 +390,179 @@ __global__ void __launch_bounds__(kSelThreads) kv_select_kernel(const __grid_con
     }
     __syncthreads();
   }
-  // keys above the threshold are kept, and the first s_want equal to it
+  // keys above the threshold are kept, and the first n_eq equal to it. The
+  // tokens of a warp lie 32 together, `blocks` of them in all; blocks are
+  // scanned 1024 at a time, thread i holding block base + i.
   const uint32_t thr = s_prefix;
   const int n_eq = s_want;
-  const int per = (old + kSelWarps * 32 - 1) / (kSelWarps * 32) * 32;  // tokens of one warp, in order
-  const int lo = warp * per, hi = min(lo + per, old);
-  int above = 0, equal = 0;
-  for (int i = lo + lane; i < hi; i += 32) {
-    const uint32_t key = mass_key(mass[i]);
-    above += key > thr;
-    equal += key == thr;
-  }
-  above = __reduce_add_sync(kFull, above);
-  equal = __reduce_add_sync(kFull, equal);
-  if (lane == 0) {
-    n_above[warp] = above;
-    n_equal[warp] = equal;
-  }
-  __syncthreads();
-  int a0 = 0, e0 = 0;
-  for (int w = 0; w < warp; ++w) {
-    a0 += n_above[w];
-    e0 += n_equal[w];
-  }
   const uint32_t below = (1u << lane) - 1u;
-  for (int i0 = lo; i0 < hi; i0 += 32) {
-    const int i = i0 + lane;
-    const uint32_t key = i < hi ? mass_key(mass[i]) : 0u;
-    const bool up = i < hi && key > thr, eq = i < hi && key == thr;
-    const uint32_t mu = __ballot_sync(kFull, up), me = __ballot_sync(kFull, eq);
-    const int na = a0 + __popc(mu & below), ne = e0 + __popc(me & below);
-    if (up || (eq && ne < n_eq)) kept[na + min(ne, n_eq)] = i;
-    a0 += __popc(mu);
-    e0 += __popc(me);
+  const int blocks = (old + 31) / 32;
+  int2* count = reinterpret_cast<int2*>(&hist[0][0]);  // 1024 pairs (above, equal)
+  int2 carry = make_int2(0, 0);
+  for (int base = 0; base < blocks; base += kSelThreads) {
+    // block base + 32 k + warp: tokens from 32 times that on, the thread's k-th key where base = 0
+    auto block_key = [&](int k, int& i) {
+      i = (base + 32 * k + warp) * 32 + lane;
+      return KEYS > 0 ? (k < HELD ? keys[k] : 0u) : i < old ? mass_key(mass[i]) : 0u;
+    };
+    constexpr int ROUNDS = KEYS > 0 ? HELD : 32;
+    count[tid] = make_int2(0, 0);
+    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < ROUNDS; ++k) {
+      int i;
+      const uint32_t key = block_key(k, i);
+      const uint32_t up = __ballot_sync(kFull, i < old && key > thr), eq = __ballot_sync(kFull, i < old && key == thr);
+      if (lane == 0) count[32 * k + warp] = make_int2(__popc(up), __popc(eq));
+    }
+    __syncthreads();
+    const int2 mine = count[tid];
+    int2 sum = mine;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const int x = __shfl_up_sync(kFull, sum.x, d), y = __shfl_up_sync(kFull, sum.y, d);
+      if (lane >= d) {
+        sum.x += x;
+        sum.y += y;
+      }
+    }
+    if (lane == 31) sums[warp] = sum;
+    __syncthreads();
+    int2 before = carry;
+    for (int w = 0; w < kSelWarps; ++w) {
+      const int2 o = sums[w];
+      if (w < warp) {
+        before.x += o.x;
+        before.y += o.y;
+      }
+      carry.x += o.x;
+      carry.y += o.y;
+    }
+    count[tid] = make_int2(before.x + sum.x - mine.x, before.y + sum.y - mine.y);
+    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < ROUNDS; ++k) {
+      int i;
+      const uint32_t key = block_key(k, i);
+      const bool up = i < old && key > thr, eq = i < old && key == thr;
+      const int2 first = count[32 * k + warp];
+      const int ne = first.y + __popc(__ballot_sync(kFull, eq) & below);
+      const int na = first.x + __popc(__ballot_sync(kFull, up) & below);
+      if (up || (eq && ne < n_eq)) kept[na + min(ne, n_eq)] = i;
+    }
+    __syncthreads();
   }
 }
 
 // Copies the kept tokens' K and V rows to the destination pages and their
-// masses to new_mass. Four lanes per token, a quarter of its code bytes each.
-// Bound by bytes: kept rows read and written once.
+// masses to new_mass. Four lanes per token, a quarter of its code bytes each;
+// kMoveTokens tokens per thread load before any is stored. Bound by bytes: kept
+// rows read and written once.
+constexpr int kMoveTokens = 2;
+template <int D>
 __global__ void __launch_bounds__(256) kv_move_kernel(const __grid_constant__ KvEvictArgs a) {
+  constexpr int W = D / 32;  // words of a quarter row
   grid_launch_dependents();
   grid_dependency_wait();
   const KvView& kv = a.src;
-  const int per_cta = 64;
-  const int chunks = (a.new_cap + per_cta - 1) / per_cta;
+  constexpr int kPerCta = 64 * kMoveTokens;
+  const int chunks = (a.new_cap + kPerCta - 1) / kPerCta;
   const int bh = blockIdx.x / chunks;
-  const int i = (blockIdx.x - bh * chunks) * per_cta + (threadIdx.x >> 2), t = threadIdx.x & 3;
+  const int i0 = (blockIdx.x - bh * chunks) * kPerCta + (threadIdx.x >> 2), t = threadIdx.x & 3;
   const int b = bh / kv.heads, h = bh - b * kv.heads;
-  if (i >= a.new_cap) return;
-  const int from = i < a.budget ? a.kept[static_cast<int64_t>(bh) * a.budget + i] : -1;
-  if (t == 0)
-    a.new_mass[b * a.new_mass_stride_b + h * a.new_mass_stride_h + i] =
-        from >= 0 ? a.mass[b * a.mass_stride_b + h * a.mass_stride_h + from] : 0.0f;
-  if (from < 0) return;
-  const uint8_t* src = kv_block(kv, b, from, h, 0);
-  uint8_t* dst = kv_block(a.dst, b, i, h, 0);
-  if (!src || !dst) {
-    if (t == 0) atomicOr(&g_status, kOpsBadPage);
-    return;
-  }
   const int half = kv.dim >> 1, ng = kv.dim / kv.group;
-  const int s0 = from & (kv.page - 1), s1 = i & (kv.page - 1);
+  int from[kMoveTokens];
+  uint8_t* dst[kMoveTokens];
+  uint32_t codes[kMoveTokens][2][W], meta[kMoveTokens][2];
+  float m[kMoveTokens];
 #pragma unroll
-  for (int which = 0; which < 2; ++which) {
-    const uint8_t* sb = src + which * kv.block_bytes;
-    uint8_t* db = dst + which * kv.block_bytes;
-    if (kv.dim == 128)
-      reinterpret_cast<uint4*>(db + s1 * half)[t] = reinterpret_cast<const uint4*>(sb + s0 * half)[t];
-    else
-      reinterpret_cast<uint2*>(db + s1 * half)[t] = reinterpret_cast<const uint2*>(sb + s0 * half)[t];
-    if (t < ng)
-      reinterpret_cast<uint32_t*>(db + kv.page * half)[s1 * ng + t] =
-          reinterpret_cast<const uint32_t*>(sb + kv.page * half)[s0 * ng + t];
+  for (int k = 0; k < kMoveTokens; ++k) {
+    const int i = i0 + 64 * k;
+    from[k] = i < a.budget ? a.kept[static_cast<int64_t>(bh) * a.budget + i] : -1;
+  }
+#pragma unroll
+  for (int k = 0; k < kMoveTokens; ++k) {
+    m[k] = 0.0f;
+    dst[k] = nullptr;
+    if (from[k] < 0) continue;
+    m[k] = a.mass[b * a.mass_stride_b + h * a.mass_stride_h + from[k]];
+    const uint8_t* src = kv_block(kv, b, from[k], h, 0);
+    dst[k] = src ? kv_block(a.dst, b, i0 + 64 * k, h, 0) : nullptr;
+    if (!dst[k]) {
+      if (t == 0) atomicOr(&g_status, kOpsBadPage);
+      continue;
+    }
+    const int slot = from[k] & (kv.page - 1);
+#pragma unroll
+    for (int which = 0; which < 2; ++which) {
+      const uint8_t* p = src + which * kv.block_bytes;
+#pragma unroll
+      for (int w = 0; w < W; w += 2) {
+        const uint2 v = *reinterpret_cast<const uint2*>(p + slot * half + (t * W + w) * 4);
+        codes[k][which][w] = v.x;
+        codes[k][which][w + 1] = v.y;
+      }
+      if (t < ng) meta[k][which] = reinterpret_cast<const uint32_t*>(p + kv.page * half)[slot * ng + t];
+    }
+  }
+#pragma unroll
+  for (int k = 0; k < kMoveTokens; ++k) {
+    const int i = i0 + 64 * k;
+    if (t == 0 && i < a.new_cap) a.new_mass[b * a.new_mass_stride_b + h * a.new_mass_stride_h + i] = m[k];
+    if (!dst[k]) continue;
+    const int slot = i & (kv.page - 1);
+#pragma unroll
+    for (int which = 0; which < 2; ++which) {
+      uint8_t* p = dst[k] + which * kv.block_bytes;
+#pragma unroll
+      for (int w = 0; w < W; w += 2)
+        *reinterpret_cast<uint2*>(p + slot * half + (t * W + w) * 4) = make_uint2(codes[k][which][w], codes[k][which][w + 1]);
+      if (t < ng) reinterpret_cast<uint32_t*>(p + kv.page * half)[slot * ng + t] = meta[k][which];
+    }
   }
 }
 
 }  // namespace
 
-cudaError_t launch_kv_append(const KvRowsArgs& a, cudaStream_t s) {
-  const int64_t threads = a.n_rows * a.kv.heads * 2 * (a.kv.dim / 8);
-  return launch_op(kv_append_kernel, dim3(static_cast<unsigned>((threads + 255) / 256)), dim3(256), 0, s, a);
+namespace {
+
+// Tokens of a CTA: up to four items per thread, but CTAs for the whole GPU first.
+int row_ctas(KvRowsArgs& a) {
+  a.groups = a.kv.dim / a.kv.group;
+  a.group_shift = a.kv.group == 128 ? 4 : a.kv.group == 64 ? 3 : 2;
+  a.per_token = Divider(static_cast<uint32_t>(a.kv.heads * (a.kv.dim / 8)));
+  a.per_sequence = Divider(static_cast<uint32_t>(a.n));
+  const int64_t items = a.n_rows * a.per_token.d;
+  int64_t per_cta = items / (148 * 8);
+  per_cta = per_cta < kRowThreads ? kRowThreads : per_cta > 4 * kRowThreads ? 4 * kRowThreads : per_cta;
+  a.cta_tokens = static_cast<int32_t>((per_cta + a.per_token.d - 1) / a.per_token.d);
+  return static_cast<int>((a.n_rows + a.cta_tokens - 1) / a.cta_tokens);
 }
 
-cudaError_t launch_kv_read(const KvRowsArgs& a, cudaStream_t s) {
-  const int64_t threads = a.n_rows * a.kv.heads * 2 * (a.kv.dim / 8);
-  return launch_op(kv_read_kernel, dim3(static_cast<unsigned>((threads + 255) / 256)), dim3(256), 0, s, a);
+}  // namespace
+
+cudaError_t launch_kv_append(KvRowsArgs a, cudaStream_t s) {
+  const dim3 grid(row_ctas(a)), block(kRowThreads);
+  return a.kv.bf16 ? launch_op(kv_append_kernel<true>, grid, block, 0, s, a) : launch_op(kv_append_kernel<false>, grid, block, 0, s, a);
+}
+
+cudaError_t launch_kv_read(KvRowsArgs a, cudaStream_t s) {
+  const dim3 grid(row_ctas(a)), block(kRowThreads);
+  if (a.f32)
+    return a.kv.bf16 ? launch_op(kv_read_kernel<true, true>, grid, block, 0, s, a) : launch_op(kv_read_kernel<false, true>, grid, block, 0, s, a);
+  return a.kv.bf16 ? launch_op(kv_read_kernel<true, false>, grid, block, 0, s, a) : launch_op(kv_read_kernel<false, false>, grid, block, 0, s, a);
 }
 
 cudaError_t launch_kv_evict(const KvEvictArgs& a, cudaStream_t s) {
-  cudaError_t e = launch_op(kv_select_kernel, dim3(a.batch * a.src.heads), dim3(kSelThreads), 0, s, a);
+  const dim3 units(a.batch * a.src.heads), threads(kSelThreads);
+  cudaError_t e = a.max_len <= 4 * kSelThreads    ? launch_op(kv_select_kernel<4>, units, threads, 0, s, a)
+                  : a.max_len <= 32 * kSelThreads ? launch_op(kv_select_kernel<32>, units, threads, 0, s, a)
+                                                  : launch_op(kv_select_kernel<0>, units, threads, 0, s, a);
   if (e != cudaSuccess) return e;
-  const int64_t chunks = (a.new_cap + 63) / 64;
-  return launch_op(kv_move_kernel, dim3(static_cast<unsigned>(chunks * a.batch * a.src.heads)), dim3(256), 0, s, a);
+  const int64_t chunks = (a.new_cap + 64 * kMoveTokens - 1) / (64 * kMoveTokens);
+  const dim3 grid(static_cast<unsigned>(chunks * a.batch * a.src.heads));
+  return a.src.dim == 128 ? launch_op(kv_move_kernel<128>, grid, dim3(256), 0, s, a)
+                          : launch_op(kv_move_kernel<64>, grid, dim3(256), 0, s, a);
 }
 
 cudaError_t take_status_kv(uint32_t* word) {

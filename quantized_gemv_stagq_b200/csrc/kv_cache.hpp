@@ -21,6 +21,21 @@ struct KvView {
   int32_t bf16;
 };
 
+// Division of numbers below 2^31 by d >= 1 without a division (Granlund and
+// Montgomery): with s = ceil(log2 d) and m = ceil(2^(31 + s) / d), x / d is
+// (x m) >> (31 + s), as m d - 2^(31 + s) < d <= 2^s.
+struct Divider {
+  uint32_t d = 1, m = 0x80000000u, shift = 0;
+  Divider() = default;
+  explicit Divider(uint32_t by) : d(by) {
+    while ((1ull << shift) < by) ++shift;
+    m = static_cast<uint32_t>(((1ull << (31 + shift)) + by - 1) / by);
+  }
+  __host__ __device__ uint32_t divide(uint32_t x) const {
+    return static_cast<uint32_t>((static_cast<uint64_t>(x) * m) >> (31 + shift));
+  }
+};
+
 struct KvRowsArgs {        // append and read
   KvView kv;
   void* k;                 // 16-bit rows (fp32 for a read with STAGQ_Y_F32)
@@ -30,6 +45,9 @@ struct KvRowsArgs {        // append and read
   const int32_t* lens;     // read only; null: no bound
   int64_t n_rows;          // batch * n
   int32_t n, f32, vec;     // tokens per sequence; fp32 output; 16-byte accesses allowed
+  // set by the launchers: tokens of a CTA, groups per row, log2 of a group's lanes
+  int32_t cta_tokens, groups, group_shift;
+  Divider per_token, per_sequence;  // items of a token; token rows of a sequence
 };
 
 struct KvAttnArgs {
@@ -72,8 +90,8 @@ struct KvAttnPlan {
 KvAttnPlan plan_kv_attention(int batch, int heads, int q_heads, int n_new, int dim, int group, int max_len, bool mass,
                              int num_sms);
 
-cudaError_t launch_kv_append(const KvRowsArgs& a, cudaStream_t s);
-cudaError_t launch_kv_read(const KvRowsArgs& a, cudaStream_t s);
+cudaError_t launch_kv_append(KvRowsArgs a, cudaStream_t s);
+cudaError_t launch_kv_read(KvRowsArgs a, cudaStream_t s);
 cudaError_t launch_kv_attention(const KvAttnArgs& a, const KvAttnPlan& p, cudaStream_t s);
 cudaError_t launch_kv_evict(const KvEvictArgs& a, cudaStream_t s);
 

@@ -82,8 +82,7 @@ KvView view_of(const stagq_kv_cache* c, const stagq_kv_table* t) {
   return v;
 }
 
-// Append and read take the same rows: their CTAs (256 threads, dim / 8 per
-// row, K and V) must fit a grid.
+// Append and read take the same rows.
 const char* rows_error(const stagq_kv_cache* c, const stagq_kv_table* t, int32_t n, const void* k, int64_t ks,
                        const void* v, int64_t vs) {
   if (const char* e = pool_error(c)) return e;
@@ -92,8 +91,7 @@ const char* rows_error(const stagq_kv_cache* c, const stagq_kv_table* t, int32_t
   if (!k || !v) return "null k or v";
   const int64_t row = static_cast<int64_t>(c->heads) * c->dim;
   if (ks < row || vs < row) return "k or v rows overlap (stride below heads * dim)";
-  if (static_cast<int64_t>(t->batch) * n > (static_cast<int64_t>(INT_MAX) * 256) / (c->heads * 2 * (c->dim / 8)))
-    return "too many rows for one call";
+  if (static_cast<int64_t>(t->batch) * n > INT_MAX) return "too many rows for one call";
   return nullptr;
 }
 
