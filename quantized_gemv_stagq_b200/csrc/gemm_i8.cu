@@ -161,6 +161,9 @@ __host__ __device__ constexpr size_t gemm_smem(int bn) {
   return 1024 + static_cast<size_t>(stage_count(bn)) * stage_bytes(bn) + kBarrierBytes;
 }
 
+__device__ __forceinline__ void prefetch_map(const CUtensorMap* map) {
+  asm volatile("prefetch.tensormap [%0];" ::"l"(map) : "memory");
+}
 __device__ __forceinline__ void tma_load_2d(uint32_t dst, const CUtensorMap* map, int x, int y, uint32_t bar) {
   asm volatile(
       "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
@@ -174,8 +177,8 @@ __device__ __forceinline__ uint64_t smem_desc(uint32_t addr) {
 }
 // kind::i8 instruction descriptor: int32 accumulator, both operands signed 8
 // bits and K-major.
-constexpr uint32_t instr_desc(int bn) {
-  return (2u << 4) | (1u << 7) | (1u << 10) | (static_cast<uint32_t>(bn >> 3) << 17) | (static_cast<uint32_t>(kBM >> 4) << 24);
+constexpr uint32_t instr_desc(int bn, int bm) {
+  return (2u << 4) | (1u << 7) | (1u << 10) | (static_cast<uint32_t>(bn >> 3) << 17) | (static_cast<uint32_t>(bm >> 4) << 24);
 }
 __device__ __forceinline__ void mma_i8(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool accumulate) {
   asm volatile(
@@ -186,6 +189,30 @@ __device__ __forceinline__ void mma_i8(uint32_t d, uint64_t a, uint64_t b, uint3
 }
 __device__ __forceinline__ void mma_commit(uint32_t bar) {
   asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
+}
+// The same on a pair of CTAs: copies that complete on the first CTA's barrier,
+// MMAs on both shared memories, commits that arrive in both CTAs.
+__device__ __forceinline__ void tma_load_2d_pair(uint32_t dst, const CUtensorMap* map, int x, int y, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
+      "l"(map), "r"(x), "r"(y), "r"(bar)
+      : "memory");
+}
+__device__ __forceinline__ void mma_i8_pair(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::2.kind::i8 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(accumulate ? 1u : 0u)
+      : "memory");
+}
+__device__ __forceinline__ void mma_commit_pair(uint32_t bar) {
+  asm volatile(
+      "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(bar),
+      "h"(static_cast<uint16_t>(3))
+      : "memory");
+}
+__device__ __forceinline__ void mbar_arrive_cluster(uint32_t bar) {
+  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 __device__ __forceinline__ void mbar_arrive(uint32_t bar) {
   asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
@@ -199,7 +226,7 @@ __device__ __forceinline__ void tmem_load16(uint32_t addr, int (&v)[16]) {
   asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
 }
 __device__ __forceinline__ void cluster_sync_all() {
-  asm volatile("barrier.cluster.arrive.aligned;\n\tbarrier.cluster.wait.aligned;" ::: "memory");
+  asm volatile("barrier.cluster.arrive;\n\tbarrier.cluster.wait;" ::: "memory");
 }
 __device__ __forceinline__ int load_peer(uint32_t addr, uint32_t rank) {
   uint32_t peer;
@@ -236,6 +263,8 @@ __global__ void __launch_bounds__(kGemmThreads) gemm_i8_kernel(const __grid_cons
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
   if (threadIdx.x == 0) {
+    prefetch_map(&wmap);
+    prefetch_map(&xmap);
     for (int s = 0; s < STAGES; ++s) {
       mbar_init(full(s), 1);
       mbar_init(empty(s), 1);
@@ -300,7 +329,7 @@ __global__ void __launch_bounds__(kGemmThreads) gemm_i8_kernel(const __grid_cons
     }
   } else if (warp == 1) {
     if (lane == 0) {
-      constexpr uint32_t idesc = instr_desc(BN);
+      constexpr uint32_t idesc = instr_desc(BN, kBM);
       uint32_t it = 0, tile = 0;
       bool ok = true;
       for (int w = first; w < n_work && ok; w += step, ++tile) {
@@ -378,10 +407,23 @@ __global__ void __launch_bounds__(kGemmThreads) gemm_i8_kernel(const __grid_cons
       const int cols = min(BN, a.n - n0);
       if (o < a.out) {
         const float ws = __ldg(a.ws + o);
-        for (int c = part; c < cols; c += a.split) {
-          int sum = 0;
-          for (int r = 0; r < a.split; ++r) sum += load_peer(ring + (c * kBM + row) * 4, r);
-          store_y(a, static_cast<int64_t>(n0 + c) * a.y_stride + o, static_cast<float>(sum) * __ldg(a.xs + n0 + c) * ws);
+        // four columns' sums of every CTA at a time: a load from a peer takes as long as one from L2
+        for (int c0 = part; c0 < cols; c0 += 4 * a.split) {
+          int v[4][8];
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int r = 0; r < 8; ++r)
+              v[i][r] = r < a.split && c0 + i * a.split < cols ? load_peer(ring + ((c0 + i * a.split) * kBM + row) * 4, r) : 0;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int c = c0 + i * a.split;
+            if (c >= cols) break;
+            int sum = 0;
+#pragma unroll
+            for (int r = 0; r < 8; ++r) sum += v[i][r];
+            store_y(a, static_cast<int64_t>(n0 + c) * a.y_stride + o, static_cast<float>(sum) * __ldg(a.xs + n0 + c) * ws);
+          }
         }
       }
     }
@@ -393,6 +435,236 @@ __global__ void __launch_bounds__(kGemmThreads) gemm_i8_kernel(const __grid_cons
   asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
   if (warp == 1)
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(tmem_cols(BN)));
+}
+
+// Many tokens: two CTAs of a cluster share a tile of 256 tokens x BN channels
+// (cta_group::2). Each loads its 128 tokens and half of the channels; the MMAs,
+// issued by the first, read both halves of the channels from both shared
+// memories. Each keeps its 128 tokens of the accumulator in its own TMEM, a
+// token per lane, so that a thread holds consecutive channels of one row of y
+// and stores 16 bytes at a time; eight warps do that under the next tile's MMAs
+// (with 2-byte stores by four warps they did not keep up with K = 4096).
+// Barriers that the MMAs wait for are the first CTA's.
+//
+// BN = 256 reads 512 rows of operands per 65536 products and K element, BN = 128
+// 384 per 32768: at K = 14336 and 4096 tokens and channels the latter was bound
+// by L2 (2.8 GB: 237 us, against 175).
+constexpr int pair_stage_bytes(int bn) { return (kBM + bn / 2) * kBK; }
+constexpr int pair_stages(int bn) { return bn == 128 ? 8 : 6; }
+constexpr size_t pair_smem(int bn) { return 1024 + static_cast<size_t>(pair_stages(bn)) * pair_stage_bytes(bn) + kBarrierBytes; }
+
+__device__ __forceinline__ uint32_t in_first_cta(uint32_t addr) {
+  uint32_t r;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(r) : "r"(addr));
+  return r;
+}
+
+constexpr int kPairThreads = 320;  // TMA warp, MMA warp, eight epilogue warps
+
+// 16 consecutive channels of 32 rows of y, a row per lane, from int32 sums.
+// `at`: the lane's first element; `left` channels exist; `rows`: lanes whose row
+// exists. Where every row is aligned to 16 bytes a lane stores its own; else the
+// warp turns the block round in shared memory and stores two rows' 16 channels at
+// a time.
+struct __align__(16) TurnBuffer {
+  float v[32][17];
+};
+__device__ __forceinline__ void store_rows(const GemmI8Args& a, int64_t at, const int (&v)[16], float xs, const float* ws,
+                                           int left, int rows, int lane, TurnBuffer& turn) {
+  float y[16];
+#pragma unroll
+  for (int i = 0; i < 16; i += 4) {
+    const float4 w = *reinterpret_cast<const float4*>(ws + i);
+    y[i] = static_cast<float>(v[i]) * xs * w.x;
+    y[i + 1] = static_cast<float>(v[i + 1]) * xs * w.y;
+    y[i + 2] = static_cast<float>(v[i + 2]) * xs * w.z;
+    y[i + 3] = static_cast<float>(v[i + 3]) * xs * w.w;
+  }
+  if (a.wide && left >= 16) {
+    if (lane >= rows) return;
+    if (a.y_f32) {
+      float4* dst = reinterpret_cast<float4*>(static_cast<float*>(a.y) + at);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) dst[i] = make_float4(y[4 * i], y[4 * i + 1], y[4 * i + 2], y[4 * i + 3]);
+    } else {
+      uint32_t p[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) p[i] = ops::pack2(ops::store16(y[2 * i], a.y_bf16), ops::store16(y[2 * i + 1], a.y_bf16));
+      uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.y) + at);
+      dst[0] = make_uint4(p[0], p[1], p[2], p[3]);
+      dst[1] = make_uint4(p[4], p[5], p[6], p[7]);
+    }
+    return;
+  }
+  __syncwarp();
+#pragma unroll
+  for (int i = 0; i < 16; ++i) turn.v[lane][i] = y[i];
+  __syncwarp();
+  const int c = lane & 15, r0 = lane >> 4;
+  const int64_t base = __shfl_sync(kFull, at, 0) + c;
+  if (c < left) {
+#pragma unroll 4
+    for (int r = r0; r < min(rows, 32); r += 2) store_y(a, base + r * a.y_stride, turn.v[r][c]);
+  }
+}
+
+template <int BN>
+__global__ void __launch_bounds__(kPairThreads) gemm_i8_pair_kernel(const __grid_constant__ GemmI8Args a,
+                                                                   const __grid_constant__ CUtensorMap wmap,
+                                                                   const __grid_constant__ CUtensorMap xmap) {
+  constexpr int STAGES = pair_stages(BN), STAGE = pair_stage_bytes(BN), ACC = 2;
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ uint32_t s_tmem;
+  __shared__ uint32_t s_stop;
+  __shared__ __align__(16) float s_ws[8][BN / 2];  // scales of an epilogue warp's channels
+  __shared__ TurnBuffer s_turn[8];
+  const uint32_t ring = (smem_addr(smem_raw) + 1023u) & ~1023u;
+  const uint32_t bars = ring + STAGES * STAGE;
+  auto full = [&](int s) { return bars + 8 * s; };
+  auto empty = [&](int s) { return bars + 8 * (STAGES + s); };
+  auto acc_full = [&](int s) { return bars + 8 * (2 * STAGES + s); };
+  auto acc_empty = [&](int s) { return bars + 8 * (2 * STAGES + ACC + s); };
+  const uint32_t drained = bars + 8 * (2 * STAGES + 2 * ACC);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int rank = blockIdx.x & 1;
+
+  if (threadIdx.x == 0) {
+    prefetch_map(&wmap);
+    prefetch_map(&xmap);
+    for (int s = 0; s < STAGES; ++s) {
+      mbar_init(full(s), 1);    // the first CTA's: both CTAs' copies complete on it
+      mbar_init(empty(s), 1);   // in both: the MMAs' commit arrives
+    }
+    for (int s = 0; s < ACC; ++s) {
+      mbar_init(acc_full(s), 1);
+      mbar_init(acc_empty(s), 512);  // the first CTA's: both CTAs' epilogue threads
+    }
+    mbar_init(drained, 1);
+    s_stop = 0;
+    fence_barrier_init();
+  }
+  if (warp == 1) {
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_addr(&s_tmem)), "r"(2 * BN)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+  }
+  asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+  __syncthreads();
+  cluster_sync_all();  // both CTAs' barriers are set up
+  asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+  const uint32_t tmem = s_tmem;
+  volatile uint32_t* stop = &s_stop;
+  grid_launch_dependents();
+  grid_dependency_wait();
+
+  const int n_work = a.m_tiles * a.n_tiles, first = blockIdx.x >> 1, step = gridDim.x >> 1;
+  auto give_up = [&]() {
+    s_stop = 1;
+    __threadfence_block();
+    atomicOr(&g_status, kOpsTimeout);
+  };
+
+  if (warp == 0) {
+    if (lane == 0) {
+      uint32_t it = 0;
+      bool ok = true;
+      for (int w = first; w < n_work && ok; w += step) {
+        const int m0 = (w % a.m_tiles) * 2 * kBM + rank * kBM, c0 = (w / a.m_tiles) * BN + rank * (BN / 2);
+        for (int k = 0; k < a.kblocks; ++k, ++it) {
+          const int s = it % STAGES;
+          if (!mbar_wait_unless(empty(s), ((it / STAGES) & 1) ^ 1, kWaitLimitNs, stop)) {
+            ok = false;
+            break;
+          }
+          const uint32_t dst = ring + s * STAGE, bar = in_first_cta(full(s));
+          if (rank == 0) mbar_arrive_expect_tx(full(s), 2 * STAGE);
+          tma_load_2d_pair(dst, &xmap, k * kBK, m0, bar);
+          tma_load_2d_pair(dst + kBM * kBK, &wmap, k * kBK, c0, bar);
+        }
+      }
+      if (!ok) {
+        give_up();
+        // the copies in flight land before either CTA's shared memory goes: the
+        // first CTA sees both CTAs', the second can only give its own a millisecond
+        if (rank == 0) {
+          for (uint32_t j = it < STAGES ? 0 : it - STAGES; j < it; ++j)
+            kernels::mbar_wait(full(j % STAGES), (j / STAGES) & 1, kWaitLimitNs);
+        } else {
+          const uint64_t t0 = kernels::global_timer();
+          while (kernels::global_timer() - t0 < 1000000) {
+          }
+        }
+      }
+    }
+  } else if (warp == 1) {
+    if (rank == 0 && lane == 0) {
+      constexpr uint32_t idesc = instr_desc(BN, 2 * kBM);
+      uint32_t it = 0, tile = 0;
+      bool ok = true;
+      for (int w = first; w < n_work && ok; w += step, ++tile) {
+        const int buf = tile % ACC;
+        if (!mbar_wait_unless(acc_empty(buf), ((tile / ACC) & 1) ^ 1, kWaitLimitNs, stop)) {
+          ok = false;
+          break;
+        }
+        asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+        for (int k = 0; k < a.kblocks; ++k, ++it) {
+          const int s = it % STAGES;
+          if (!mbar_wait_unless(full(s), (it / STAGES) & 1, kWaitLimitNs, stop)) {
+            ok = false;
+            break;
+          }
+          asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+          const uint64_t ad = smem_desc(ring + s * STAGE), bd = smem_desc(ring + s * STAGE + kBM * kBK);
+#pragma unroll
+          for (int i = 0; i < kBK / 32; ++i) mma_i8_pair(tmem + buf * BN, ad + 2 * i, bd + 2 * i, idesc, k > 0 || i > 0);
+          mma_commit_pair(empty(s));
+        }
+        if (ok) mma_commit_pair(acc_full(buf));
+      }
+      if (!ok) {
+        give_up();
+        mma_commit_pair(drained);  // no MMA may still read the rings or write TMEM when the CTAs go
+        kernels::mbar_wait(drained, 0, kWaitLimitNs);
+      }
+    }
+  } else {
+    const int quarter = warp & 3, half = (warp - 2) >> 2;
+    float* scales = s_ws[warp - 2];
+    uint32_t tile = 0;
+    for (int w = first; w < n_work; w += step, ++tile) {
+      const int tok = (w % a.m_tiles) * 2 * kBM + rank * kBM + quarter * 32 + lane;
+      const int o0 = (w / a.m_tiles) * BN + half * (BN / 2);
+      const int buf = tile % ACC;
+      __syncwarp();
+#pragma unroll
+      for (int i = lane; i < BN / 2; i += 32) scales[i] = o0 + i < a.out ? __ldg(a.ws + o0 + i) : 0.0f;
+      __syncwarp();
+      bool ok = mbar_wait_unless(acc_full(buf), (tile / ACC) & 1, kWaitLimitNs, stop);
+      ok = __all_sync(kFull, ok);
+      if (!ok) {
+        if (lane == 0) give_up();
+        break;
+      }
+      asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+      const uint32_t addr = tmem + buf * BN + half * (BN / 2) + (static_cast<uint32_t>(quarter * 32) << 16);
+      const float xs = tok < a.n ? __ldg(a.xs + tok) : 0.0f;
+      const int64_t row = static_cast<int64_t>(tok) * a.y_stride;
+      const int rows = a.n - (tok - lane);  // that exist from the warp's first on
+      for (int c = 0; c < BN / 2 && o0 + c < a.out; c += 16) {
+        int v[16];
+        tmem_load16(addr + c, v);
+        store_rows(a, row + o0 + c, v, xs, scales + c, a.out - o0 - c, rows, lane, s_turn[warp - 2]);
+      }
+      asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+      mbar_arrive_cluster(in_first_cta(acc_empty(buf)));
+    }
+  }
+  asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+  __syncthreads();
+  cluster_sync_all();  // neither CTA's memory goes while the other's MMAs or copies use it
+  asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+  if (warp == 1) asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(2 * BN));
 }
 
 using EncodeTiled = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*,
@@ -423,49 +695,63 @@ bool encode_rows(CUtensorMap* map, const int8_t* p, int64_t rows, int ld, int bo
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int BN>
-cudaError_t launch_bn(const GemmI8Args& a, const GemmI8Plan& p, const CUtensorMap& wmap, const CUtensorMap& xmap,
-                      cudaStream_t s) {
+using GemmKernel = void (*)(GemmI8Args, CUtensorMap, CUtensorMap);
+
+cudaError_t launch_gemm(GemmKernel kernel, size_t smem, int cluster, const GemmI8Args& a, const GemmI8Plan& p,
+                        const CUtensorMap& wmap, const CUtensorMap& xmap, cudaStream_t s) {
   // per device and cheap; must be set before the first launch on each
-  cudaError_t e = cudaFuncSetAttribute(gemm_i8_kernel<BN>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       static_cast<int>(gemm_smem(BN)));
+  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(p.grid);
-  cfg.blockDim = dim3(kGemmThreads);
-  cfg.dynamicSmemBytes = gemm_smem(BN);
+  cfg.blockDim = dim3(p.pair ? kPairThreads : kGemmThreads);
+  cfg.dynamicSmemBytes = smem;
   cfg.stream = s;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   attr[1].id = cudaLaunchAttributeClusterDimension;
-  attr[1].val.clusterDim.x = p.split;
+  attr[1].val.clusterDim.x = cluster;
   attr[1].val.clusterDim.y = 1;
   attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
-  return cudaLaunchKernelEx(&cfg, gemm_i8_kernel<BN>, a, wmap, xmap);
+  return cudaLaunchKernelEx(&cfg, kernel, a, wmap, xmap);
 }
 
 }  // namespace
 
-// The smallest tile that holds the tokens up to 128, then 256 if that fills
-// the SMs as well. Up to 64 tokens the CTAs of a tile are doubled while all of
-// them still fit the GPU (two per SM) and keep four K blocks each.
+// Up to 64 tokens: the smallest tile that holds them, and clusters as wide as
+// all CTAs still fit the GPU (two per SM) with four K blocks each. Above, the
+// cheaper of that with 64-token tiles and of the pairs, by what was measured: a
+// K block takes a pair 0.36 us (BN = 256) or 0.29 us (BN = 128), a 64-token CTA
+// 2 ns for every CTA there is (what L2 delivers), 0.15 us at least, and the two
+// kernels 5.3 and 7.5 us besides. (256 x 14336 x 4096: 28.6 us with 64-token
+// tiles, 36.8 with pairs; 512 x 4096 x 4096: 18.1 and 15.6.)
 GemmI8Plan plan_gemm_i8(int n, int out, int kblocks, int num_sms) {
   GemmI8Plan p{};
   const int64_t m_tiles = (out + kBM - 1) / kBM;
-  auto tiles = [&](int bn) { return m_tiles * ((n + bn - 1) / bn); };
+  p.bn = n <= 16 ? 16 : n <= 32 ? 32 : 64;
   p.split = 1;
-  if (n <= 64) {
-    p.bn = n <= 16 ? 16 : n <= 32 ? 32 : 64;
-    while (p.split < 8 && tiles(p.bn) * p.split * 2 <= 2 * num_sms && kblocks >= 4 * p.split * 2) p.split *= 2;
-    p.grid = static_cast<int>(tiles(p.bn) * p.split);
-    return p;
-  }
-  const int64_t w128 = (tiles(128) + num_sms - 1) / num_sms, w256 = (tiles(256) + num_sms - 1) / num_sms;
-  p.bn = w128 <= 2 * w256 - 1 ? 128 : 256;
-  p.grid = static_cast<int>(std::min<int64_t>(tiles(p.bn), num_sms));
+  const int64_t tiles = m_tiles * ((n + p.bn - 1) / p.bn);
+  while (p.split < 8 && tiles * p.split * 2 <= 2 * num_sms && kblocks >= 4 * p.split * 2) p.split *= 2;
+  p.grid = static_cast<int>(std::min<int64_t>(tiles * p.split, 1 << 30));
+  if (n <= 64) return p;
+
+  const int64_t pairs = num_sms / 2, m_pairs = (n + 2 * kBM - 1) / (2 * kBM);
+  auto pair_tiles = [&](int bn) { return m_pairs * ((out + bn - 1) / bn); };
+  auto pair_us = [&](int bn, double block_us) {
+    return 5.3 + (pair_tiles(bn) + pairs - 1) / pairs * kblocks * block_us;
+  };
+  const double us256 = pair_us(256, 0.36), us128 = pair_us(128, 0.29);
+  const double ctas = static_cast<double>(std::min<int64_t>(tiles * p.split, 2 * num_sms));
+  const double us64 = 7.5 + static_cast<double>((tiles * p.split + 2 * num_sms - 1) / (2 * num_sms)) *
+                      ((kblocks + p.split - 1) / p.split) * std::max(0.15, 0.002 * ctas);
+  if (us64 <= us128 && us64 <= us256) return p;
+  p.split = 1;
+  p.pair = 1;
+  p.bn = us128 < us256 ? 128 : 256;
+  p.grid = static_cast<int>(2 * std::min<int64_t>(pair_tiles(p.bn), pairs));
   return p;
 }
 
@@ -490,18 +776,26 @@ cudaError_t launch_quantize_i8(const QuantizeI8Args& a, cudaStream_t s) {
 cudaError_t launch_gemm_i8(GemmI8Args a, const GemmI8Plan& p, const int8_t* xq, const int8_t* wq, int ld,
                            cudaStream_t s, bool* encode_failed) {
   a.kblocks = ld / kBK;
-  a.m_tiles = (a.out + kBM - 1) / kBM;
-  a.n_tiles = (a.n + p.bn - 1) / p.bn;
+  if (p.pair) {
+    a.m_tiles = (a.n + 2 * kBM - 1) / (2 * kBM);
+    a.n_tiles = (a.out + p.bn - 1) / p.bn;
+  } else {
+    a.m_tiles = (a.out + kBM - 1) / kBM;
+    a.n_tiles = (a.n + p.bn - 1) / p.bn;
+  }
   a.split = p.split;
+  a.wide = reinterpret_cast<uintptr_t>(a.y) % 16 == 0 && a.y_stride * (a.y_f32 ? 4 : 2) % 16 == 0;
   CUtensorMap wmap, xmap;
-  *encode_failed = !encode_rows(&wmap, wq, a.out, ld, kBM) || !encode_rows(&xmap, xq, a.n, ld, p.bn);
+  *encode_failed = !encode_rows(&wmap, wq, a.out, ld, p.pair ? p.bn / 2 : kBM) || !encode_rows(&xmap, xq, a.n, ld, p.pair ? kBM : p.bn);
   if (*encode_failed) return cudaSuccess;
+  if (p.pair) {
+    if (p.bn == 128) return launch_gemm(gemm_i8_pair_kernel<128>, pair_smem(128), 2, a, p, wmap, xmap, s);
+    return launch_gemm(gemm_i8_pair_kernel<256>, pair_smem(256), 2, a, p, wmap, xmap, s);
+  }
   switch (p.bn) {
-    case 16: return launch_bn<16>(a, p, wmap, xmap, s);
-    case 32: return launch_bn<32>(a, p, wmap, xmap, s);
-    case 64: return launch_bn<64>(a, p, wmap, xmap, s);
-    case 128: return launch_bn<128>(a, p, wmap, xmap, s);
-    default: return launch_bn<256>(a, p, wmap, xmap, s);
+    case 16: return launch_gemm(gemm_i8_kernel<16>, gemm_smem(16), p.split, a, p, wmap, xmap, s);
+    case 32: return launch_gemm(gemm_i8_kernel<32>, gemm_smem(32), p.split, a, p, wmap, xmap, s);
+    default: return launch_gemm(gemm_i8_kernel<64>, gemm_smem(64), p.split, a, p, wmap, xmap, s);
   }
 }
 

@@ -20,7 +20,10 @@ struct GemmI8Args {
   void* y;
   int64_t y_stride;   // elements between rows
   int32_t n, out, kblocks;           // kblocks: 128-byte blocks of a row
-  int32_t m_tiles, n_tiles, split;   // tiles of 128 channels and of BN tokens; CTAs of a cluster that share one
+  // tiles of 128 channels and of BN tokens, and the CTAs of a cluster that
+  // share one; for pairs, tiles of 256 tokens and of BN channels
+  int32_t m_tiles, n_tiles, split;
+  int32_t wide;                      // every row of y is aligned to 16 bytes
   int32_t y_f32, y_bf16;
 };
 
@@ -28,6 +31,7 @@ struct GemmI8Args {
 struct GemmI8Plan {
   int bn;     // tokens per tile
   int split;  // CTAs of a cluster that share a tile's K
+  int pair;   // two CTAs share a tile of 256 channels
   int grid;
 };
 
