@@ -489,7 +489,7 @@ __device__ __forceinline__ void store_rows(const GemmI8Args& a, int64_t at, cons
     } else {
       uint32_t p[8];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) p[i] = ops::pack2(ops::store16(y[2 * i], a.y_bf16), ops::store16(y[2 * i + 1], a.y_bf16));
+      for (int i = 0; i < 8; ++i) p[i] = ops::store16x2(y[2 * i], y[2 * i + 1], a.y_bf16);
       uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.y) + at);
       dst[0] = make_uint4(p[0], p[1], p[2], p[3]);
       dst[1] = make_uint4(p[4], p[5], p[6], p[7]);

@@ -69,6 +69,7 @@ using kernels::kFull;
 constexpr int kWarps = 4;
 constexpr int kTile = 32;            // tokens of a warp's tile
 constexpr int kMaxCluster = 8;
+constexpr int kMassTokens = 2048;   // tokens of a CTA of the join that adds to the mass
 
 __device__ __forceinline__ float ex2(float x) {
   float y;
@@ -697,12 +698,12 @@ __global__ void __launch_bounds__(kWarps * 32, resident_ctas(NT, NG)) kv_attenti
     const int tok = r / a.per;
     uint16_t* out = a.out + (static_cast<int64_t>(b) * a.n_new + tok) * a.out_stride + (h * a.per + r - tok * a.per) * D + d;
     const float f = den == 0.0f ? 0.0f : 1.0f / den;
-    const uint16_t y[4] = {ops::store16(sum.x * f, BF), ops::store16(sum.y * f, BF), ops::store16(sum.z * f, BF), ops::store16(sum.w * f, BF)};
+    const uint32_t y[2] = {ops::store16x2(sum.x * f, sum.y * f, BF), ops::store16x2(sum.z * f, sum.w * f, BF)};
     if (a.vec_out) {
-      *reinterpret_cast<uint2*>(out) = make_uint2(ops::pack2(y[0], y[1]), ops::pack2(y[2], y[3]));
+      *reinterpret_cast<uint2*>(out) = make_uint2(y[0], y[1]);
     } else {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) out[i] = y[i];
+      for (int i = 0; i < 4; ++i) out[i] = static_cast<uint16_t>(y[i >> 1] >> (16 * (i & 1)));
     }
   };
   for (int idx = threadIdx.x; idx < ROWS * D / 4; idx += kWarps * 32) {
@@ -785,8 +786,8 @@ __global__ void __launch_bounds__(kWarps * 32, resident_ctas(NT, NG)) kv_attenti
 }
 
 // Joins the partial sums: CTAs before n_units * ROWS each write one output row;
-// the others (tracked calls) add the weights exp2(S - lse) of 512 tokens of one
-// (sequence, head) to the mass, every element by one thread in one order.
+// the others (tracked calls) add the weights exp2(S - lse) of kMassTokens tokens
+// of one (sequence, head) to the mass, every element by one thread in one order.
 template <int D, int ROWS>
 __global__ void __launch_bounds__(512) kv_join_kernel(const __grid_constant__ KvAttnArgs a) {
   constexpr int GROUPS = 512 / D;  // partial sums read at a time
@@ -856,21 +857,33 @@ __global__ void __launch_bounds__(512) kv_join_kernel(const __grid_constant__ Kv
         ops::store16(den == 0.0f ? 0.0f : sum / den, kv.bf16);
     return;
   }
-  const int chunks = (a.max_len + 511) / 512;
+  const int chunks = (a.max_len + kMassTokens - 1) / kMassTokens;
   const int which = static_cast<int>(blockIdx.x - static_cast<int64_t>(n_units) * ROWS);
-  const int bh = which / chunks, tok = (which - bh * chunks) * 512 + threadIdx.x;
+  const int bh = which / chunks, t0 = (which - bh * chunks) * kMassTokens;
   const int b = bh / kv.heads, h = bh - b * kv.heads;
   const int len = clamped_len(a, b);
-  if (tok - static_cast<int>(threadIdx.x) >= len) return;
-  // the scores of the first rows load while their denominators are found
-  const float* scores = a.scores + static_cast<int64_t>(bh) * a.rows_pad * a.score_stride + tok;
-  constexpr int EARLY = 8;
-  float early[EARLY];
+  if (t0 >= len) return;
+  // a thread's tokens: t0 + threadIdx.x + 512 i. Four rows' scores, the first
+  // of them while the rows' denominators are found.
+  constexpr int PER = kMassTokens / 512;
+  const float* scores = a.scores + static_cast<int64_t>(bh) * a.rows_pad * a.score_stride + t0 + threadIdx.x;
+  float s[4][PER], sum[PER], old[PER];
+  auto load_rows = [&](int r0) {
 #pragma unroll
-  for (int r = 0; r < EARLY; ++r) early[r] = r < a.rows && tok < row_limit(a, len, r) ? scores[r * a.score_stride] : -INFINITY;
-  float old = 0.0f;
-  float* mass = a.mass + b * a.mass_stride_b + h * a.mass_stride_h + tok;
-  if (tok < len) old = *mass;
+    for (int r = 0; r < 4; ++r) {
+      const int limit = r0 + r < a.rows ? row_limit(a, len, r0 + r) : 0;
+#pragma unroll
+      for (int i = 0; i < PER; ++i)
+        s[r][i] = t0 + static_cast<int>(threadIdx.x) + 512 * i < limit ? scores[(r0 + r) * a.score_stride + 512 * i] : -INFINITY;
+    }
+  };
+  load_rows(0);
+  float* mass = a.mass + b * a.mass_stride_b + h * a.mass_stride_h + t0 + threadIdx.x;
+#pragma unroll
+  for (int i = 0; i < PER; ++i) {
+    old[i] = t0 + static_cast<int>(threadIdx.x) + 512 * i < len ? mass[512 * i] : 0.0f;
+    sum[i] = 0.0f;
+  }
   const int lane = threadIdx.x & 31;
   for (int r = threadIdx.x >> 5; r < a.rows; r += 16) {
     const int rb = r / ROWS, row = r - rb * ROWS;
@@ -898,17 +911,22 @@ __global__ void __launch_bounds__(512) kv_join_kernel(const __grid_constant__ Kv
         top = now;
       }
     }
-    if (lane == 0) s_lse[r] = (top == -INFINITY ? 0.0f : top) + log2f(den);
+    // (a row that sees nothing: its scores are all -inf, whatever stands here)
+    if (lane == 0) s_lse[r] = den == 0.0f ? 0.0f : (top == -INFINITY ? 0.0f : top) + log2f(den);
   }
   __syncthreads();
-  if (tok >= len) return;
-  float sum = 0.0f;
+  for (int r0 = 0; r0 < a.rows; r0 += 4) {
+    if (r0) load_rows(r0);
 #pragma unroll
-  for (int r = 0; r < EARLY; ++r)
-    if (r < a.rows && tok < row_limit(a, len, r)) sum += ex2(early[r] - s_lse[r]);
-  for (int r = EARLY; r < a.rows; ++r)
-    if (tok < row_limit(a, len, r)) sum += ex2(scores[r * a.score_stride] - s_lse[r]);
-  *mass = old + sum;
+    for (int r = 0; r < 4; ++r) {
+      const float lse = s_lse[min(r0 + r, a.rows - 1)];
+#pragma unroll
+      for (int i = 0; i < PER; ++i) sum[i] += ex2(s[r][i] - lse);
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < PER; ++i)
+    if (t0 + static_cast<int>(threadIdx.x) + 512 * i < len) mass[512 * i] = old[i] + sum[i];
 }
 
 template <int D, int NG, int NT, bool BF>
@@ -932,7 +950,7 @@ cudaError_t launch_attention(const KvAttnArgs& a, cudaStream_t s) {
   e = cudaLaunchKernelEx(&cfg, kv_attention_kernel<D, NG, NT, BF>, a);
   if (e != cudaSuccess || !a.part_o) return e;
   int64_t join = static_cast<int64_t>(a.batch) * a.kv.heads * a.row_blocks * 4 * NT;
-  if (a.scores) join += static_cast<int64_t>(a.batch) * a.kv.heads * ((a.max_len + 511) / 512);
+  if (a.scores) join += static_cast<int64_t>(a.batch) * a.kv.heads * ((a.max_len + kMassTokens - 1) / kMassTokens);
   return launch_op(kv_join_kernel<D, 4 * NT>, dim3(static_cast<unsigned>(join)), dim3(512), 0, s, a);
 }
 

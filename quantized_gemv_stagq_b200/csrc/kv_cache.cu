@@ -233,15 +233,14 @@ __device__ __forceinline__ void write8(void* base, int64_t at, uint32_t word, ui
     }
   } else {
     uint16_t* dst = static_cast<uint16_t*>(base) + at;
-    uint16_t y[8];
+    uint32_t y[4];
 #pragma unroll
-    for (int k = 0; k < 8; ++k) y[k] = ops::store16(x[k], BF);
+    for (int k = 0; k < 4; ++k) y[k] = ops::store16x2(x[2 * k], x[2 * k + 1], BF);
     if (vec) {
-      *reinterpret_cast<uint4*>(dst) =
-          make_uint4(ops::pack2(y[0], y[1]), ops::pack2(y[2], y[3]), ops::pack2(y[4], y[5]), ops::pack2(y[6], y[7]));
+      *reinterpret_cast<uint4*>(dst) = make_uint4(y[0], y[1], y[2], y[3]);
     } else {
 #pragma unroll
-      for (int k = 0; k < 8; ++k) dst[k] = y[k];
+      for (int k = 0; k < 8; ++k) dst[k] = static_cast<uint16_t>(y[k >> 1] >> (16 * (k & 1)));
     }
   }
 }

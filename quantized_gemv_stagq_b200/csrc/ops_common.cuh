@@ -30,6 +30,15 @@ __device__ __forceinline__ float load16(uint16_t v, bool bf16) {
 __device__ __forceinline__ uint16_t store16(float v, bool bf16) {
   return bf16 ? __bfloat16_as_ushort(__float2bfloat16_rn(v)) : __half_as_ushort(__float2half_rn(v));
 }
+// Two values rounded and packed by one instruction, lo in the lower half.
+__device__ __forceinline__ uint32_t store16x2(float lo, float hi, bool bf16) {
+  uint32_t r;
+  if (bf16)
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  else
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
 // binary64 to fp16 or bf16 with one rounding: to fp32 by round-to-odd (a
 // truncation whose lost bits set the last one), which keeps a tie a tie and a
 // near tie a near tie, then to nearest even. fp32 has 13 bits more than fp16.
