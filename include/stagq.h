@@ -450,7 +450,7 @@ int64_t stagq_kv_page_bytes(const stagq_kv_cache* cache);
 /*
  * Rounds n new tokens of every sequence to 4 bits and writes them at positions
  * starts[b] .. starts[b] + n - 1. Row b * n + i of k and v ([heads * dim]
- * values, k_stride / v_stride elements apart) is token i of sequence b. A
+ * values, k_stride / v_stride elements apart, below 2^31) is token i of sequence b. A
  * sequence with starts[b] < 0 is left alone (padding of a batch). A position
  * past the table's width, or whose page number is not in the pool, is not
  * written and is reported by stagq_ops_check (STAGQ_EFORMAT).

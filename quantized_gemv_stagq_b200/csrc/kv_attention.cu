@@ -35,8 +35,8 @@
 //
 // A warp takes 32 tokens at a time. Each has a ring of tiles in shared memory
 // of its own, filled by bulk copies (4 per tile, one per lane, 8 where a page
-// holds half a tile) two tiles ahead: no registers wait for memory, so 16 warps
-// fit an SM. The four warps of a CTA take tiles in turn and join their sums at
+// holds half a tile) one tile ahead: no registers wait for memory, so 12
+// warps of 168 registers fit an SM. The four warps of a CTA take tiles in turn and join their sums at
 // the end; nothing in the loop waits for another warp.
 //
 // The work is cut into rounds of 128 tokens (a tile per warp) of a unit
@@ -135,11 +135,13 @@ __device__ __forceinline__ void load_words(uint32_t (&w)[WORDS], const uint8_t* 
   }
 }
 
-// CTAs that fit an SM by their registers: 128 a thread hold 4 query rows and
-// one group per head without spilling, more groups need 168, 8 rows 255.
-constexpr int resident_ctas(int nt, int groups) { return nt > 1 ? 2 : groups > 1 ? 3 : 4; }
+// CTAs of an SM: 168 registers a thread for 4 query rows, 255 for 8. (With 128
+// registers 4 CTAs fit and one group per head does not spill, but 16 ragged
+// sequences up to 8192 tokens then took 33.1 us instead of 31.9: the runs of
+// tiles are shorter against what starts and ends them.)
+constexpr int resident_ctas(int nt) { return nt > 1 ? 2 : 3; }
 
-constexpr int kStages = 3;
+constexpr int kStages = 2;
 constexpr uint64_t kWaitLimitNs = 2000000000ull;
 
 // A tile in shared memory: codes of K and of V (32 rows of D / 2 bytes each),
@@ -207,7 +209,7 @@ __device__ __forceinline__ float4 load_peer4(uint32_t addr, uint32_t rank) {
 }
 
 template <int D, int NG, int NT, bool BF>
-__global__ void __launch_bounds__(kWarps * 32, resident_ctas(NT, NG)) kv_attention_kernel(const __grid_constant__ KvAttnArgs a) {
+__global__ void __launch_bounds__(kWarps * 32, resident_ctas(NT)) kv_attention_kernel(const __grid_constant__ KvAttnArgs a) {
   constexpr int J = D / 32;       // blocks of 32 channels
   constexpr int JG = J / NG;      // blocks of a group
   constexpr int ROWS = 4 * NT;
@@ -337,7 +339,7 @@ __global__ void __launch_bounds__(kWarps * 32, resident_ctas(NT, NG)) kv_attenti
     __syncwarp();
     if (copies)
       kernels::bulk_load(ring_addr + s * L::kBytes + copy_dst,
-                         head + (ok ? pid : 0) * kv.page_stride + ((i * kTile + piece * piece_tokens) & (kv.page - 1)) * row_bytes,
+                         head + static_cast<uint64_t>(static_cast<uint32_t>(ok ? pid : 0)) * kv.page_stride + ((i * kTile + piece * piece_tokens) & (kv.page - 1)) * row_bytes,
                          copy_bytes, full_addr + 8 * s);
     ++filled;
   };
@@ -972,7 +974,7 @@ int64_t align256(int64_t v) { return (v + 255) / 256 * 256; }
 // longest sequence; the even split takes an equal share of all rounds (of a
 // batch, about 0.6 times the longest sequence's each), and a second launch of
 // about 5 us.
-KvAttnPlan plan_kv_attention(int batch, int heads, int q_heads, int n_new, int dim, int group, int max_len, bool mass,
+KvAttnPlan plan_kv_attention(int batch, int heads, int q_heads, int n_new, int dim, int max_len, bool mass,
                              int num_sms) {
   KvAttnPlan p{};
   const int rows = q_heads / heads * n_new;
@@ -981,7 +983,7 @@ KvAttnPlan plan_kv_attention(int batch, int heads, int q_heads, int n_new, int d
   p.rows_pad = p.row_blocks * 4 * p.nt;
   const int64_t units = static_cast<int64_t>(batch) * heads * p.row_blocks;
   const int64_t rounds = (static_cast<int64_t>(max_len) + kWarps * kTile - 1) / (kWarps * kTile);
-  const int64_t fit = static_cast<int64_t>(num_sms) * resident_ctas(p.nt, dim / group);
+  const int64_t fit = static_cast<int64_t>(num_sms) * resident_ctas(p.nt);
   p.score_stride = mass ? rounds * kWarps * kTile : 0;
   if (!mass) {
     int64_t s = 1;

@@ -12,6 +12,8 @@
 // lane, see kv_attention.cu): a K row holds channel 32 j + 8 t + n in nibble n
 // of the 4 bytes at t dim / 8 + 4 j (t = 0..3); a V row holds channel
 // 32 j + 4 g + n in nibble n of the 2 bytes at g dim / 16 + 2 j (g = 0..7).
+#include <climits>
+
 #include "kv_cache.hpp"
 #include "kernel_common.cuh"
 #include "ops_common.cuh"
@@ -25,13 +27,15 @@ using kernels::grid_dependency_wait;
 using kernels::grid_launch_dependents;
 using kernels::kFull;
 
-// Block of (page of position pos, head, which) of sequence b; null if the
-// position or the page number is outside the table or the pool.
-__device__ __forceinline__ uint8_t* kv_block(const KvView& kv, int64_t b, int64_t pos, int head, int which) {
-  if (pos < 0 || (pos >> kv.page_shift) >= kv.table_width) return nullptr;
-  const int pid = kv.table[b * kv.table_stride + (pos >> kv.page_shift)];
+// K block of (page of position pos, head) of sequence b; null if the position
+// or the page number is outside the table or the pool. The sizes of a pool's
+// parts fit 32 bits, so that each offset is one widening multiplication.
+__device__ __forceinline__ uint8_t* kv_block(const KvView& kv, int b, int pos, int head) {
+  const int page = pos >> kv.page_shift;
+  if (pos < 0 || page >= kv.table_width) return nullptr;
+  const int pid = kv.table[b * kv.table_stride + page];
   if (pid < 0 || pid >= kv.n_pages) return nullptr;
-  return kv.pages + static_cast<int64_t>(pid) * kv.page_stride + static_cast<int64_t>(2 * head + which) * kv.block_bytes;
+  return kv.pages + static_cast<uint64_t>(static_cast<uint32_t>(pid)) * kv.page_stride + static_cast<uint32_t>(2 * head * kv.block_bytes);
 }
 
 // Append and read: dim / 8 lanes take a token's K and V rows of one head, 8
@@ -50,6 +54,12 @@ __device__ __forceinline__ Item item_of(const KvRowsArgs& a, int tok0, uint32_t 
 }
 
 constexpr int kRowThreads = 256;
+
+__device__ __forceinline__ uint64_t row_offset(int row, uint32_t stride) {
+  return static_cast<uint64_t>(static_cast<uint32_t>(row)) * stride;
+}
+// start + i, which stays past every table where it would overflow.
+__device__ __forceinline__ int position(int start, int i) { return start > INT_MAX - i ? INT_MAX : start + i; }
 constexpr float kWhole = 12582912.0f;  // 1.5 * 2^23: a sum with it is rounded to a whole number
 
 // ------------------------------------------------------------------ append
@@ -186,12 +196,12 @@ __global__ void __launch_bounds__(kRowThreads) kv_append_kernel(const __grid_con
     const bool in = i < n_items;
     const Item it = item_of(a, tok0, in ? i : 0);
     const int c = it.head * kv.dim + 8 * it.c8;
-    const uint4 k = load8_packed(static_cast<const uint16_t*>(a.k) + it.tok * a.k_stride + c, a.vec);
-    const uint4 v = load8_packed(static_cast<const uint16_t*>(a.v) + it.tok * a.v_stride + c, a.vec);
+    const uint4 k = load8_packed(static_cast<const uint16_t*>(a.k) + row_offset(it.tok, a.k_stride) + c, a.vec);
+    const uint4 v = load8_packed(static_cast<const uint16_t*>(a.v) + row_offset(it.tok, a.v_stride) + c, a.vec);
     const int b = static_cast<int>(a.per_sequence.divide(it.tok));
     const int start = a.starts[b];
-    const int64_t pos = start < 0 ? -1 : static_cast<int64_t>(start) + (it.tok - b * a.n);
-    uint8_t* block = kv_block(kv, b, pos, it.head, 0);
+    const int pos = position(start, it.tok - b * a.n);
+    uint8_t* block = kv_block(kv, b, start < 0 ? -1 : pos, it.head);
     if (in && !block && start >= 0 && it.c8 == 0) atomicOr(&g_status, kOpsBadPage);
     uint32_t pair_k, pair_v;
     const uint32_t word_k = round8<BF>(k, glanes, pair_k), word_v = round8<BF>(v, glanes, pair_v);
@@ -200,7 +210,7 @@ __global__ void __launch_bounds__(kRowThreads) kv_append_kernel(const __grid_con
     const uint32_t other = __shfl_xor_sync(kFull, word_v, 4);
     const uint32_t bytes_v = j & 1 ? __byte_perm(other, word_v, 0x7632) : __byte_perm(word_v, other, 0x5410);
     if (!in || !block) continue;
-    const int slot = static_cast<int>(pos & (kv.page - 1)), half = kv.dim >> 1;
+    const int slot = pos & (kv.page - 1), half = kv.dim >> 1;
     uint8_t* at = block + slot * half;
     *reinterpret_cast<uint32_t*>(at + t * (kv.dim >> 3) + 4 * j) = word_k;
     at += kv.block_bytes;
@@ -259,13 +269,13 @@ __global__ void __launch_bounds__(kRowThreads) kv_read_kernel(const __grid_const
   for (uint32_t i = threadIdx.x; i < n_items; i += kRowThreads) {
     const Item it = item_of(a, tok0, i);
     const int b = static_cast<int>(a.per_sequence.divide(it.tok));
-    const int64_t pos = static_cast<int64_t>(a.starts ? a.starts[b] : 0) + (it.tok - b * a.n);
+    const int pos = position(a.starts ? a.starts[b] : 0, it.tok - b * a.n);
     const bool inside = pos >= 0 && (!a.lens || pos < a.lens[b]);
-    const uint8_t* block = inside ? kv_block(kv, b, pos, it.head, 0) : nullptr;
+    const uint8_t* block = inside ? kv_block(kv, b, pos, it.head) : nullptr;
     if (inside && !block && it.c8 == 0) atomicOr(&g_status, kOpsBadPage);
     uint32_t word_k = 0, word_v = 0, pair_k = 0, pair_v = 0;
     if (block) {
-      const int slot = static_cast<int>(pos & (kv.page - 1));
+      const int slot = pos & (kv.page - 1);
       const int j = it.c8 >> 2, t = it.c8 & 3;
       const uint8_t* at = block + slot * half;
       word_k = *reinterpret_cast<const uint32_t*>(at + t * (kv.dim >> 3) + 4 * j);
@@ -277,8 +287,8 @@ __global__ void __launch_bounds__(kRowThreads) kv_read_kernel(const __grid_const
       pair_v = *reinterpret_cast<const uint32_t*>(meta + kv.block_bytes);
     }
     const int c = it.head * kv.dim + 8 * it.c8;
-    write8<BF, F32>(a.k, it.tok * a.k_stride + c, word_k, pair_k, a.vec);
-    write8<BF, F32>(a.v, it.tok * a.v_stride + c, word_v, pair_v, a.vec);
+    write8<BF, F32>(a.k, row_offset(it.tok, a.k_stride) + c, word_k, pair_k, a.vec);
+    write8<BF, F32>(a.v, row_offset(it.tok, a.v_stride) + c, word_v, pair_v, a.vec);
   }
 }
 
@@ -485,8 +495,8 @@ __global__ void __launch_bounds__(256) kv_move_kernel(const __grid_constant__ Kv
     dst[k] = nullptr;
     if (from[k] < 0) continue;
     m[k] = a.mass[b * a.mass_stride_b + h * a.mass_stride_h + from[k]];
-    const uint8_t* src = kv_block(kv, b, from[k], h, 0);
-    dst[k] = src ? kv_block(a.dst, b, i0 + 64 * k, h, 0) : nullptr;
+    const uint8_t* src = kv_block(kv, b, from[k], h);
+    dst[k] = src ? kv_block(a.dst, b, i0 + 64 * k, h) : nullptr;
     if (!dst[k]) {
       if (t == 0) atomicOr(&g_status, kOpsBadPage);
       continue;

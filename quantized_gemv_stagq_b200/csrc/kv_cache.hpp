@@ -15,7 +15,7 @@ struct KvView {
   uint8_t* pages;
   const int32_t* table;
   int64_t table_stride;    // entries between the table rows of two sequences
-  int64_t page_stride;     // bytes of a page (all heads, K and V)
+  uint32_t page_stride;    // bytes of a page (all heads, K and V)
   int32_t block_bytes;     // bytes of a (page, head, K | V) block
   int32_t n_pages, table_width, heads, dim, group, page, page_shift;
   int32_t bf16;
@@ -23,7 +23,8 @@ struct KvView {
 
 // Division of numbers below 2^31 by d >= 1 without a division (Granlund and
 // Montgomery): with s = ceil(log2 d) and m = ceil(2^(31 + s) / d), x / d is
-// (x m) >> (31 + s), as m d - 2^(31 + s) < d <= 2^s.
+// (x m) >> (31 + s), as m d - 2^(31 + s) < d <= 2^s; that is the upper word of
+// 2 x m, shifted by s.
 struct Divider {
   uint32_t d = 1, m = 0x80000000u, shift = 0;
   Divider() = default;
@@ -31,16 +32,16 @@ struct Divider {
     while ((1ull << shift) < by) ++shift;
     m = static_cast<uint32_t>(((1ull << (31 + shift)) + by - 1) / by);
   }
-  __host__ __device__ uint32_t divide(uint32_t x) const {
-    return static_cast<uint32_t>((static_cast<uint64_t>(x) * m) >> (31 + shift));
-  }
+#ifdef __CUDACC__
+  __device__ __forceinline__ uint32_t divide(uint32_t x) const { return __umulhi(2 * x, m) >> shift; }
+#endif
 };
 
 struct KvRowsArgs {        // append and read
   KvView kv;
   void* k;                 // 16-bit rows (fp32 for a read with STAGQ_Y_F32)
   void* v;
-  int64_t k_stride, v_stride;  // elements between two rows
+  uint32_t k_stride, v_stride;  // elements between two rows
   const int32_t* starts;   // null: 0
   const int32_t* lens;     // read only; null: no bound
   int64_t n_rows;          // batch * n
@@ -87,7 +88,7 @@ struct KvAttnPlan {
   int64_t off_ml, off_o, off_unit, off_scores, bytes;  // workspace layout
 };
 
-KvAttnPlan plan_kv_attention(int batch, int heads, int q_heads, int n_new, int dim, int group, int max_len, bool mass,
+KvAttnPlan plan_kv_attention(int batch, int heads, int q_heads, int n_new, int dim, int max_len, bool mass,
                              int num_sms);
 
 cudaError_t launch_kv_append(KvRowsArgs a, cudaStream_t s);

@@ -70,7 +70,7 @@ KvView view_of(const stagq_kv_cache* c, const stagq_kv_table* t) {
   v.table = t->pages;
   v.table_stride = t->row_stride;
   v.block_bytes = c->page * (c->dim / 2 + 4 * (c->dim / c->group));
-  v.page_stride = 2 * static_cast<int64_t>(c->heads) * v.block_bytes;
+  v.page_stride = 2u * c->heads * v.block_bytes;  // at most 2 * 4096 * 1024 * 80 bytes
   v.n_pages = c->n_pages;
   v.table_width = t->width;
   v.heads = c->heads;
@@ -91,6 +91,7 @@ const char* rows_error(const stagq_kv_cache* c, const stagq_kv_table* t, int32_t
   if (!k || !v) return "null k or v";
   const int64_t row = static_cast<int64_t>(c->heads) * c->dim;
   if (ks < row || vs < row) return "k or v rows overlap (stride below heads * dim)";
+  if (ks > INT_MAX || vs > INT_MAX) return "k or v rows lie 2^31 elements apart or more";
   if (static_cast<int64_t>(t->batch) * n > INT_MAX) return "too many rows for one call";
   return nullptr;
 }
@@ -182,8 +183,8 @@ extern "C" int stagq_kv_append(const stagq_kv_cache* c, const stagq_kv_table* t,
   a.kv = view_of(c, t);
   a.k = const_cast<void*>(k);
   a.v = const_cast<void*>(v);
-  a.k_stride = k_stride;
-  a.v_stride = v_stride;
+  a.k_stride = static_cast<uint32_t>(k_stride);
+  a.v_stride = static_cast<uint32_t>(v_stride);
   a.starts = starts;
   a.n = n;
   a.n_rows = static_cast<int64_t>(t->batch) * n;
@@ -202,8 +203,8 @@ extern "C" int stagq_kv_read(const stagq_kv_cache* c, const stagq_kv_table* t, c
   a.kv = view_of(c, t);
   a.k = k;
   a.v = v;
-  a.k_stride = k_stride;
-  a.v_stride = v_stride;
+  a.k_stride = static_cast<uint32_t>(k_stride);
+  a.v_stride = static_cast<uint32_t>(v_stride);
   a.starts = starts;
   a.lens = lens;
   a.n = n;
@@ -243,7 +244,7 @@ extern "C" int64_t stagq_kv_attention_workspace(const stagq_kv_cache* c, int32_t
     set_error("no usable device");
     return -1;
   }
-  return plan_kv_attention(batch, c->heads, q_heads, n_new, c->dim, c->group, max_len, tracked != 0, sms).bytes;
+  return plan_kv_attention(batch, c->heads, q_heads, n_new, c->dim, max_len, tracked != 0, sms).bytes;
 }
 
 extern "C" int stagq_kv_attention(const stagq_kv_cache* c, const stagq_kv_table* t, const int32_t* lens,
@@ -264,7 +265,7 @@ extern "C" int stagq_kv_attention(const stagq_kv_cache* c, const stagq_kv_table*
   if (!guard.ok) return fail(STAGQ_ECUDA, "cudaSetDevice failed");
   const int sms = sm_count(c->device);
   if (!sms) return fail(STAGQ_ENODEV, "no usable device");
-  const KvAttnPlan p = plan_kv_attention(t->batch, c->heads, q_heads, n_new, c->dim, c->group, max_len, mass != nullptr, sms);
+  const KvAttnPlan p = plan_kv_attention(t->batch, c->heads, q_heads, n_new, c->dim, max_len, mass != nullptr, sms);
   if (p.bytes && (!workspace || !aligned(workspace, 256) || workspace_bytes < p.bytes))
     return bad("workspace must be 256-byte aligned and hold stagq_kv_attention_workspace() bytes");
   KvAttnArgs a{};

@@ -102,7 +102,7 @@ def test_kv_refuses_bad_arguments_before_any_device_work():
     for kw in BAD_TABLES:
         t = Q._KvTable(*{**tab, **kw}.values())
         assert rows(t=t) == (EINVAL, EINVAL) and attend(t=t) == EINVAL and evict(t=t) == EINVAL and evict(f=t) == EINVAL, kw
-    for kw in (dict(k=None), dict(v=None), dict(ks=255), dict(vs=255), dict(n=0), dict(n=2 ** 30 + 1)):
+    for kw in (dict(k=None), dict(v=None), dict(ks=255), dict(vs=255), dict(ks=2 ** 31), dict(vs=2 ** 31), dict(n=0), dict(n=2 ** 30 + 1)):
         assert rows(**kw) == (EINVAL, EINVAL), kw
     assert rows(starts=None)[0] == EINVAL
     assert L.stagq_kv_read(r(good), r(table), None, None, p, row, p, row, 1, 2, None) == EINVAL
