@@ -16,7 +16,8 @@ are in ``per_launch``.
 
   python bench.py [--gpus N] [--steps K] [--warmup W] [--impl stagq|reference]
                   [--workload llama31_8b_linears_b1 | phi4_olmo2_linears_b1 | precision_sweep |
-                              llama31_8b_stack | llama31_8b_guarded | cublas_context]
+                              llama31_8b_stack | llama31_8b_guarded | llama31_8b_layer |
+                              cublas_context]
 
 The default workload is the Llama-3.1-8B layer above. The others print one
 JSON line each with per-GEMV (or per-token) times:
@@ -29,6 +30,11 @@ JSON line each with per-GEMV (or per-token) times:
   llama31_8b_guarded     the Llama-3.1-8B linears at group 32 with the paper's
                          side-record guards (ratio T = 4 + post-grid), each
                          alone and as a layer chain;
+  llama31_8b_layer       one Llama-3.1-8B layer's decode step with its attention:
+                         q/k/v GEMV, append to and attention over the 4-bit
+                         cache, o, gate/up and down, at contexts of 1024, 8192
+                         and 32768 tokens, batch 1 and 4; and the layer's
+                         linears in 8 bits for a 512-token prompt;
   precision_sweep        14336x4096 and 4096x14336 with base + 4 planes, read at
                          2..6 bits, group 16, 32, 64 and 128, side record
                          0 / 0.1 / 1 %;
@@ -72,7 +78,7 @@ def _args():
     p.add_argument("--no-cpu-baseline", action="store_true")
     p.add_argument("--workload", default=WORKLOAD,
                    choices=[WORKLOAD, "phi4_olmo2_linears_b1", "precision_sweep", "llama31_8b_stack",
-                            "llama31_8b_guarded", "cublas_context"])
+                            "llama31_8b_guarded", "llama31_8b_layer", "cublas_context"])
     p.add_argument("--stack-distinct", type=int, default=4,
                    help="llama31_8b_stack: distinct encoded layers (the 32 resident layers cycle over them)")
     return p.parse_args()
@@ -451,6 +457,79 @@ def run_extra(args):
         cfg = {"linears_out_x_in": {k: list(v) for k, v in shapes}, "bits": list(BITS), "group": 32,
                "n_planes": N_PLANES, "side_record": "pre-grid ratio guard T = 4 + post-grid guard (1 per row)",
                "batch": 1}
+    elif args.workload == "llama31_8b_layer":
+        heads, q_heads, dim, page, group, bits = 8, 32, 128, 64, 128, 4
+        enc = {n: Q.stagq_pack(Q.stagq_encode(synth.weights(o, i, seed=j), GROUP, N_PLANES, DENSITY, "fast"))
+               for j, (n, (o, i)) in enumerate(_layer_shapes())}
+        mats = {name: Q.stagq_load_stack([enc[n] for n in members], 0) for name, members in LAYER_LAUNCHES}
+        row = 2 * heads * (dim // 2 + 4 * (dim // group))  # a cached token's bytes, K and V
+
+        def graph_us(body, reps):
+            with torch.cuda.stream(stream):
+                body()
+            torch.cuda.synchronize()
+            g = torch.cuda.CUDAGraph()
+            with torch.cuda.graph(g, stream=stream):
+                for _ in range(reps):
+                    body()
+            return _median_event_us(torch, stream, g.replay, 5) / reps
+
+        for batch in (1, 4):
+            x = {n: torch.from_numpy(synth.activations(batch, m.inp, seed=m.inp)).cuda() for n, m in mats.items()}
+            y = {n: torch.empty(batch, m.out, dtype=torch.float16, device="cuda") for n, m in mats.items()}
+            q, k, v = y["qkv"].split([q_heads * dim, heads * dim, heads * dim], 1)
+            for ctx in (1024, 8192, 32768):
+                per = ctx // page
+                pages = torch.zeros(batch * per, Q.stagq_kv_page_bytes(heads, dim, page, group), dtype=torch.uint8, device="cuda")
+                cache = Q.KVCache(pages, heads, dim, page, group, torch.float16)
+                table = torch.randperm(batch * per, dtype=torch.int32, device="cuda").view(batch, per)
+                starts = torch.zeros(batch, dtype=torch.int32, device="cuda")
+                kv = torch.randn(batch * ctx, heads * dim, device="cuda").half()
+                Q.stagq_kv_append(cache, kv, kv.flip(0), table, starts, ctx)
+                starts += ctx - 1
+                lens, ws = starts + 1, torch.empty(Q.stagq_kv_attention_workspace(cache, batch, ctx, q_heads),
+                                                   dtype=torch.uint8, device="cuda")
+                torch.cuda.synchronize()
+
+                def attention():
+                    Q.stagq_kv_append(cache, k, v, table, starts, 1, stream=stream)
+                    Q.stagq_kv_attention(cache, q, table, lens, x["o"], workspace=ws, stream=stream)
+
+                def step():
+                    Q.stagq_gemv_n(mats["qkv"], bits, x["qkv"], batch, y["qkv"], stream=stream)
+                    attention()
+                    for n in ("o", "gate_up", "down"):
+                        Q.stagq_gemv_n(mats[n], bits, x[n], batch, y[n], stream=stream)
+
+                nb = batch * ctx * row
+                for what, us, n in (("attention", graph_us(attention, 20), nb),
+                                    ("step", graph_us(step, 20), nb + sum(Q.stagq_bytes(m, bits, batch) for m in mats.values()))):
+                    launches += 21 * 6 * 6
+                    results[f"{what} batch{batch} ctx{ctx}"] = {"us": round(us, 2), "bytes": n, "gbs": round(n / us / 1e3, 1),
+                                                                "frac": round(n / us / 1e3 / peak, 4)}
+        n = 512
+        for name, m in mats.items():
+            w = torch.randn(m.out, m.inp, device="cuda").mul_(0.02).half()
+            wq, wscale = torch.empty(m.out, m.inp, dtype=torch.int8, device="cuda"), torch.empty(m.out, device="cuda")
+            Q.stagq_quantize_i8(w, wq, wscale)
+            xi = torch.from_numpy(synth.activations(n, m.inp, seed=n)).cuda()
+            xq, xscale = torch.empty(n, m.inp, dtype=torch.int8, device="cuda"), torch.empty(n, device="cuda")
+            yi = torch.empty(n, m.out, dtype=torch.float16, device="cuda")
+            torch.cuda.synchronize()
+
+            def linear():
+                Q.stagq_quantize_i8(xi, xq, xscale, stream=stream)
+                Q.stagq_gemm_i8(xq, xscale, wq, wscale, m.inp, yi, stream=stream)
+
+            us = graph_us(linear, 20)
+            launches += 2 * 21 * 6
+            nb = 2 * n * m.inp + m.out * m.inp + 2 * n * m.out
+            results[f"i8 {name} {m.out}x{m.inp} tokens{n}"] = {
+                "us": round(us, 2), "bytes": nb, "tflops": round(2e-6 * n * m.inp * m.out / us, 1),
+                "gbs": round(nb / us / 1e3, 1), "frac": round(nb / us / 1e3 / peak, 4)}
+        cfg = {"linears_out_x_in": {k: list(v) for k, v in _layer_shapes()}, "bits": bits, "group": GROUP, "q_heads": q_heads,
+               "kv_heads": heads, "head_dim": dim, "cache": "4 bits, groups of 128, pages of 64 tokens", "batches": [1, 4],
+               "note": "one layer repeated in a CUDA graph: its weights and, at short contexts, its cache stay in L2"}
     elif args.workload == "precision_sweep":
         shapes = [("gate", (14336, 4096)), ("down", (4096, 14336))]
         for g in (16, 32, 64, 128):

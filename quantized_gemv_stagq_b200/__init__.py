@@ -730,9 +730,11 @@ def stagq_kv_attention(cache: KVCache, q, table, lens, out, n_new: int = 1, scal
             raise ValueError(f"workspace must be contiguous and on cuda:{dev}")
     elif need:
         import torch
-        workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
-        if stream is not None:  # the allocator must not reuse it while `stream` still does
-            workspace.record_stream(torch.cuda.ExternalStream(s, device=dev))
+        if s == _raw_stream(dev):
+            workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+        else:  # memory that is free for the call's own stream, not for torch's current one
+            with torch.cuda.stream(torch.cuda.ExternalStream(s, device=dev) if s else torch.cuda.default_stream(dev)):
+                workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
     _check(lib().stagq_kv_attention(cache._c, t, at_lens, max_len, q.data_ptr(), qs, q_heads, n_new,
                                     cache.dim ** -0.5 if scale is None else scale, out.data_ptr(), outs,
                                     None if mass is None else mass.data_ptr(), mb, mh,
