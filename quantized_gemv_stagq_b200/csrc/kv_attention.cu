@@ -50,7 +50,7 @@
 //    device, so that a ragged batch, one long sequence and many short ones fill
 //    the GPU alike. A unit that one CTA covers is written out; the others leave
 //    a partial sum (at most two per CTA), and a second kernel joins those.
-#include <climits>
+#include <algorithm>
 #include <cmath>
 
 #include "kernel_common.cuh"
@@ -967,8 +967,8 @@ int64_t align256(int64_t v) { return (v + 255) / 256 * 256; }
 }  // namespace
 
 // Four query rows of a KV head per unit, eight where there are more than four
-// (the cache is then read once per eight rows). A round takes about 1 us in a
-// CTA that has its SM to itself and 4 us where all of them are full. Clusters
+// (the cache is then read once per eight rows). A round takes about 1.4 us in a
+// CTA that has its SM to itself and 2.2 us where all of them are full. Clusters
 // of S CTAs per unit (S up to 8, no more than the rounds, all resident at once
 // where that goes) take ceil(rounds / S) rounds after one another, of the
 // longest sequence; the even split takes an equal share of all rounds (of a
@@ -988,7 +988,7 @@ KvAttnPlan plan_kv_attention(int batch, int heads, int q_heads, int n_new, int d
   if (!mass) {
     int64_t s = 1;
     while (s < kMaxCluster && s < rounds && units * s * 2 <= fit) s *= 2;
-    auto round_us = [&](int64_t ctas) { return ctas >= fit ? 4.0 : ctas * 4 <= fit ? 1.0 : 4.0 * ctas / fit; };
+    auto round_us = [&](int64_t ctas) { return std::max(1.4, 2.2 * std::min<int64_t>(ctas, fit) / fit); };
     const double waves = static_cast<double>((units * s + fit - 1) / fit);
     const double clusters_us = waves * static_cast<double>((rounds + s - 1) / s) * round_us(units * s);
     const double work = static_cast<double>(units * rounds) * (batch > 1 ? 0.6 : 1.0);
