@@ -715,7 +715,7 @@ cudaError_t launch_gemm(GemmKernel kernel, size_t smem, int cluster, const GemmI
   attr[1].val.clusterDim.y = 1;
   attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 2;
+  cfg.numAttrs = cluster > 1 ? 2 : 1;
   return cudaLaunchKernelEx(&cfg, kernel, a, wmap, xmap);
 }
 

@@ -948,7 +948,7 @@ cudaError_t launch_attention(const KvAttnArgs& a, cudaStream_t s) {
   attr[1].val.clusterDim.x = a.cluster > 1 ? a.cluster : 1;
   attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 2;
+  cfg.numAttrs = a.cluster > 1 ? 2 : 1;
   e = cudaLaunchKernelEx(&cfg, kv_attention_kernel<D, NG, NT, BF>, a);
   if (e != cudaSuccess || !a.part_o) return e;
   int64_t join = static_cast<int64_t>(a.batch) * a.kv.heads * a.row_blocks * 4 * NT;

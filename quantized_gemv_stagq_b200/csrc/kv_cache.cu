@@ -304,44 +304,69 @@ __device__ __forceinline__ uint32_t mass_key(float m) {
   return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
 }
 
-// kept[b, h, :] for one (sequence, head) per CTA: the `want` largest masses of
-// the first `old` tokens, ties to the lowest index, then the recent tokens, all
-// in their order. A radix selection finds the want-th largest key 8 bits at a
-// time; every lane counts into its own copy of the histogram (256 x 32
-// counters), so equal keys, which a mass of mostly one exponent is full of, do
-// not queue on one shared-memory word. Then every 32 tokens count their kept
-// ones, a scan over the counts numbers them, and the kept positions are written.
-// Up to KEYS * 1024 tokens are read once and stay in registers; KEYS = 0 reads
-// them again in each of the six passes (they come from L2).
+__device__ __forceinline__ void cluster_sync_all() {
+  asm volatile("barrier.cluster.arrive;\n\tbarrier.cluster.wait;" ::: "memory");
+}
+__device__ __forceinline__ int load_peer(const int* p, uint32_t rank) {
+  uint32_t peer;
+  int v;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(peer) : "r"(kernels::smem_addr(p)), "r"(rank));
+  asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(v) : "r"(peer) : "memory");
+  return v;
+}
+
+// kept[b, h, :] for one (sequence, head) per cluster of a.share CTAs: the `want`
+// largest masses of the first `old` tokens, ties to the lowest index, then the
+// recent tokens, all in their order. The CTAs take consecutive slices of the
+// tokens. A radix selection finds the want-th largest key 8 bits at a time;
+// every lane counts into its own copy of the histogram (256 x 32 counters), so
+// equal keys, which a mass of mostly one exponent is full of, do not queue on
+// one shared-memory word, and the CTAs add their histograms through distributed
+// shared memory. Then every 32 tokens count their kept ones, a scan over the
+// counts and the CTAs numbers them, and the kept positions are written. Up to
+// KEYS * 1024 tokens of a slice are read once and stay in registers; KEYS = 0
+// (share 1) reads them again in each of the six passes (they come from L2).
+// Bound by instructions, 6 passes of about 10 a key, hence the sharing: 64
+// heads of 32768 tokens, moved too, take 38 us with one CTA each and 30 with two.
 template <int KEYS>
 __global__ void __launch_bounds__(kSelThreads) kv_select_kernel(const __grid_constant__ KvEvictArgs a) {
   __shared__ int hist[kBins][32];
-  __shared__ int total[kBins];
+  __shared__ int total[2][kBins];  // of this CTA, in turn by pass: peers may still read the last one's
+  __shared__ int all[kBins];
   __shared__ int2 sums[kSelWarps];
+  __shared__ int s_kept[2];        // this CTA's tokens above the threshold, and equal to it
   __shared__ uint32_t s_prefix;
   __shared__ int s_want;
   grid_launch_dependents();
   grid_dependency_wait();
-  const int b = blockIdx.x / a.src.heads, h = blockIdx.x - b * a.src.heads;
+  const int unit = blockIdx.x / a.share, rank = blockIdx.x - unit * a.share;
+  const int b = unit / a.src.heads, h = unit - b * a.src.heads;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   int len = a.lens[b];
   if (len > a.max_len || len < 0) {
     if (tid == 0) atomicOr(&g_status, kOpsBadPage);
     len = len < 0 ? 0 : a.max_len;
   }
-  int32_t* kept = a.kept + static_cast<int64_t>(blockIdx.x) * a.budget;
+  int32_t* kept = a.kept + static_cast<int64_t>(unit) * a.budget;
   const int n_kept = min(len, a.budget);
-  if (h == 0 && tid == 0) a.new_lens[b] = n_kept;
-  for (int i = n_kept + tid; i < a.budget; i += kSelThreads) kept[i] = -1;
-  if (len <= a.budget) {
-    for (int i = tid; i < len; i += kSelThreads) kept[i] = i;
-    return;
+  if (rank == 0) {
+    if (h == 0 && tid == 0) a.new_lens[b] = n_kept;
+    for (int i = n_kept + tid; i < a.budget; i += kSelThreads) kept[i] = -1;
   }
-  const int old = len - a.recent, want = a.budget - a.recent;
-  for (int i = tid; i < a.recent; i += kSelThreads) kept[want + i] = old + i;
-  if (want == 0) return;
+  // (the CTAs of a cluster leave together: at once, or after the last barrier)
+  const int old_all = len - a.recent, want = a.budget - a.recent;
+  const bool select = len > a.budget && want > 0;
+  if (rank == 0) {
+    if (len <= a.budget)
+      for (int i = tid; i < len; i += kSelThreads) kept[i] = i;
+    else
+      for (int i = tid; i < a.recent; i += kSelThreads) kept[want + i] = old_all + i;
+  }
+  if (a.share == 1 && !select) return;
 
-  const float* mass = a.mass + b * a.mass_stride_b + h * a.mass_stride_h;
+  const int per = select ? (old_all + 32 * a.share - 1) / (32 * a.share) * 32 : 0;
+  const int first = select ? min(rank * per, old_all) : 0, old = select ? min(per, old_all - first) : 0;
+  const float* mass = a.mass + b * a.mass_stride_b + h * a.mass_stride_h + first;
   constexpr int HELD = KEYS > 0 ? KEYS : 1;
   uint32_t keys[HELD];
   if (KEYS > 0) {
@@ -351,7 +376,7 @@ __global__ void __launch_bounds__(kSelThreads) kv_select_kernel(const __grid_con
       keys[k] = i < old ? mass_key(mass[i]) : 0u;
     }
   }
-  // f(token, key) for the thread's tokens: tid, tid + 1024, ...
+  // f(key) for the thread's tokens: tid, tid + 1024, ... of the slice
   auto each = [&](auto&& f) {
     if (KEYS > 0) {
 #pragma unroll
@@ -366,6 +391,7 @@ __global__ void __launch_bounds__(kSelThreads) kv_select_kernel(const __grid_con
     s_want = want;
   }
   for (int shift = 24; shift >= 0; shift -= 8) {
+    int* mine_total = total[(shift >> 3) & 1];
     for (int i = tid; i < kBins * 32; i += kSelThreads) (&hist[0][0])[i] = 0;
     __syncthreads();
     const uint32_t prefix = s_prefix, mask = shift == 24 ? 0u : 0xFFFFFFFFu << (shift + 8);
@@ -376,13 +402,23 @@ __global__ void __launch_bounds__(kSelThreads) kv_select_kernel(const __grid_con
     __syncthreads();
     for (int i = warp; i < kBins; i += kSelWarps) {
       const int n = __reduce_add_sync(kFull, hist[i][lane]);
-      if (lane == 0) total[i] = n;
+      if (lane == 0) mine_total[i] = n;
+    }
+    const int* sum_total = mine_total;
+    if (a.share > 1) {
+      cluster_sync_all();
+      if (tid < kBins) {
+        int n = 0;
+        for (int r = 0; r < a.share; ++r) n += load_peer(mine_total + tid, r);
+        all[tid] = n;
+      }
+      sum_total = all;
     }
     __syncthreads();
     if (warp == 0) {  // lane l: bins 255 - 8 l .. 248 - 8 l, from the largest down
       int mine = 0;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) mine += total[255 - 8 * lane - i];
+      for (int i = 0; i < 8; ++i) mine += sum_total[255 - 8 * lane - i];
       int before = mine;
 #pragma unroll
       for (int d = 1; d < 32; d <<= 1) {
@@ -390,9 +426,9 @@ __global__ void __launch_bounds__(kSelThreads) kv_select_kernel(const __grid_con
         if (lane >= d) before += o;
       }
       before -= mine;
-      if (before < left && before + mine >= left) {  // one lane
+      if (before < left && before + mine >= left) {  // one lane (none if nothing is selected)
         int bin = 255 - 8 * lane;
-        while (before + total[bin] < left) before += total[bin--];
+        while (before + sum_total[bin] < left) before += sum_total[bin--];
         s_prefix = prefix | (static_cast<uint32_t>(bin) << shift);
         s_want = left - before;
       }
@@ -408,7 +444,9 @@ __global__ void __launch_bounds__(kSelThreads) kv_select_kernel(const __grid_con
   const int blocks = (old + 31) / 32;
   int2* count = reinterpret_cast<int2*>(&hist[0][0]);  // 1024 pairs (above, equal)
   int2 carry = make_int2(0, 0);
-  for (int base = 0; base < blocks; base += kSelThreads) {
+  // With several CTAs there is one round of blocks, and the CTAs before this
+  // one have kept `carry` first.
+  for (int base = 0; base < max(blocks, 1); base += kSelThreads) {
     // block base + 32 k + warp: tokens from 32 times that on, the thread's k-th key where base = 0
     auto block_key = [&](int k, int& i) {
       i = (base + 32 * k + warp) * 32 + lane;
@@ -437,30 +475,44 @@ __global__ void __launch_bounds__(kSelThreads) kv_select_kernel(const __grid_con
     }
     if (lane == 31) sums[warp] = sum;
     __syncthreads();
-    int2 before = carry;
+    int2 before = make_int2(0, 0), whole = make_int2(0, 0);
     for (int w = 0; w < kSelWarps; ++w) {
       const int2 o = sums[w];
       if (w < warp) {
         before.x += o.x;
         before.y += o.y;
       }
-      carry.x += o.x;
-      carry.y += o.y;
+      whole.x += o.x;
+      whole.y += o.y;
     }
-    count[tid] = make_int2(before.x + sum.x - mine.x, before.y + sum.y - mine.y);
+    if (a.share > 1) {
+      if (tid == 0) {
+        s_kept[0] = whole.x;
+        s_kept[1] = whole.y;
+      }
+      cluster_sync_all();
+      for (int r = 0; r < rank; ++r) {
+        carry.x += load_peer(&s_kept[0], r);
+        carry.y += load_peer(&s_kept[1], r);
+      }
+    }
+    count[tid] = make_int2(carry.x + before.x + sum.x - mine.x, carry.y + before.y + sum.y - mine.y);
+    carry.x += whole.x;
+    carry.y += whole.y;
     __syncthreads();
 #pragma unroll
     for (int k = 0; k < ROUNDS; ++k) {
       int i;
       const uint32_t key = block_key(k, i);
       const bool up = i < old && key > thr, eq = i < old && key == thr;
-      const int2 first = count[32 * k + warp];
-      const int ne = first.y + __popc(__ballot_sync(kFull, eq) & below);
-      const int na = first.x + __popc(__ballot_sync(kFull, up) & below);
-      if (up || (eq && ne < n_eq)) kept[na + min(ne, n_eq)] = i;
+      const int2 at = count[32 * k + warp];
+      const int ne = at.y + __popc(__ballot_sync(kFull, eq) & below);
+      const int na = at.x + __popc(__ballot_sync(kFull, up) & below);
+      if (up || (eq && ne < n_eq)) kept[na + min(ne, n_eq)] = first + i;
     }
     __syncthreads();
   }
+  if (a.share > 1) cluster_sync_all();  // no CTA leaves while a peer reads its counts
 }
 
 // Copies the kept tokens' K and V rows to the destination pages and their
@@ -562,11 +614,43 @@ cudaError_t launch_kv_read(KvRowsArgs a, cudaStream_t s) {
   return a.kv.bf16 ? launch_op(kv_read_kernel<true, false>, grid, block, 0, s, a) : launch_op(kv_read_kernel<false, false>, grid, block, 0, s, a);
 }
 
-cudaError_t launch_kv_evict(const KvEvictArgs& a, cudaStream_t s) {
-  const dim3 units(a.batch * a.src.heads), threads(kSelThreads);
-  cudaError_t e = a.max_len <= 4 * kSelThreads    ? launch_op(kv_select_kernel<4>, units, threads, 0, s, a)
-                  : a.max_len <= 32 * kSelThreads ? launch_op(kv_select_kernel<32>, units, threads, 0, s, a)
-                                                  : launch_op(kv_select_kernel<0>, units, threads, 0, s, a);
+namespace {
+
+template <int KEYS>
+cudaError_t launch_select(const KvEvictArgs& a, cudaStream_t s) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(a.batch * a.src.heads * a.share);
+  cfg.blockDim = dim3(kSelThreads);
+  cfg.stream = s;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = a.share;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = a.share > 1 ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, kv_select_kernel<KEYS>, a);
+}
+
+}  // namespace
+
+// CTAs of a selection: doubled while they fit the GPU and keep more than 4096
+// tokens each, and while a slice does not fit the registers (up to 8).
+cudaError_t launch_kv_evict(KvEvictArgs a, int num_sms, cudaStream_t s) {
+  const int64_t units = static_cast<int64_t>(a.batch) * a.src.heads;
+  a.share = 1;
+  while (a.share < 8 && ((units * a.share * 2 <= num_sms && a.max_len > a.share * 2 * 4096) || a.max_len > a.share * 32 * kSelThreads))
+    a.share *= 2;
+  int64_t slice = (static_cast<int64_t>(a.max_len) + 32 * a.share - 1) / (32 * a.share) * 32;
+  if (slice > 32 * kSelThreads || units * a.share > (1 << 30)) {
+    a.share = 1;
+    slice = a.max_len;
+  }
+  cudaError_t e = slice <= 4 * kSelThreads    ? launch_select<4>(a, s)
+                  : slice <= 16 * kSelThreads ? launch_select<16>(a, s)
+                  : slice <= 32 * kSelThreads ? launch_select<32>(a, s)
+                                              : launch_select<0>(a, s);
   if (e != cudaSuccess) return e;
   const int64_t chunks = (a.new_cap + 64 * kMoveTokens - 1) / (64 * kMoveTokens);
   const dim3 grid(static_cast<unsigned>(chunks * a.batch * a.src.heads));

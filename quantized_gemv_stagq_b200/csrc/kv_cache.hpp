@@ -79,6 +79,7 @@ struct KvEvictArgs {
   int32_t* new_lens;
   int64_t mass_stride_b, mass_stride_h, new_mass_stride_b, new_mass_stride_h;
   int32_t batch, max_len, budget, recent, new_cap;
+  int32_t share;           // set by the launcher: CTAs that share a head's selection
 };
 
 struct KvAttnPlan {
@@ -94,6 +95,6 @@ KvAttnPlan plan_kv_attention(int batch, int heads, int q_heads, int n_new, int d
 cudaError_t launch_kv_append(KvRowsArgs a, cudaStream_t s);
 cudaError_t launch_kv_read(KvRowsArgs a, cudaStream_t s);
 cudaError_t launch_kv_attention(const KvAttnArgs& a, const KvAttnPlan& p, cudaStream_t s);
-cudaError_t launch_kv_evict(const KvEvictArgs& a, cudaStream_t s);
+cudaError_t launch_kv_evict(KvEvictArgs a, int num_sms, cudaStream_t s);
 
 }  // namespace stagq

@@ -343,7 +343,9 @@ extern "C" int stagq_kv_evict(const stagq_kv_cache* c, const stagq_kv_table* t, 
   a.budget = budget;
   a.recent = recent;
   a.new_cap = new_cap;
-  return launched(launch_kv_evict(a, static_cast<cudaStream_t>(cuda_stream)), "evict launch");
+  const int sms = sm_count(c->device);
+  if (!sms) return fail(STAGQ_ENODEV, "no usable device");
+  return launched(launch_kv_evict(a, sms, static_cast<cudaStream_t>(cuda_stream)), "evict launch");
 }
 
 extern "C" int stagq_ops_check(int device) {

@@ -631,6 +631,39 @@ def test_evict_on_equal_and_long_masses():
 
 
 @gpu
+@pytest.mark.parametrize("lens,budget,recent", [([70000, 3, 900], 900, 33), ([33000], 20000, 0), ([300000], 700, 700), ([300000], 1000, 17)])
+def test_evict_of_long_sequences(lens, budget, recent):
+    # selections shared by several CTAs, one sequence that is copied whole among them, and one too long for the registers
+    b, page, heads = len(lens), 1024, 2
+    per, fresh_per = -(-max(lens) // page), -(-budget // page)
+    size = Q.stagq_kv_page_bytes(heads, 64, page, 64)
+    pool = torch.randint(0, 60, (b * (per + fresh_per), size), dtype=torch.uint8, device="cuda")
+    cache = Q.KVCache(pool, heads, 64, page, 64, F16)
+    order = torch.randperm(b * (per + fresh_per), generator=torch.Generator().manual_seed(4)).to(torch.int32).cuda()
+    table, fresh = order[:b * per].view(b, per), order[b * per:].view(b, fresh_per)
+    mass = torch.rand(b, heads, per * page, generator=torch.Generator().manual_seed(5))
+    mass[:, 1] = torch.floor(mass[:, 1] * 50)  # ties across the CTAs' slices
+    n = torch.tensor(lens, dtype=torch.int32, device="cuda")
+    kept, new_lens = torch.empty(b, heads, budget, dtype=torch.int32, device="cuda"), torch.empty(b, dtype=torch.int32, device="cuda")
+    new_mass = torch.empty(b, heads, budget, device="cuda")
+    Q.stagq_kv_evict(cache, table, n, mass.cuda(), fresh, budget, recent, kept, new_lens, new_mass)
+    Q.stagq_ops_check(0)
+    rows = max(lens)
+    old_k, old_v = (torch.empty(b * rows, heads * 64, device="cuda") for _ in range(2))
+    Q.stagq_kv_read(cache, table, n, old_k, old_v, rows)
+    k, v = (torch.empty(b * budget, heads * 64, device="cuda") for _ in range(2))
+    Q.stagq_kv_read(cache, fresh, new_lens, k, v, budget)
+    for i in range(b):
+        for h in range(heads):
+            want = R.keep(mass[i, h].numpy(), lens[i], budget, recent)
+            assert kept[i, h].tolist() == want + [-1] * (budget - len(want))
+            at = torch.tensor(want, device="cuda")
+            for new, old in ((k, old_k), (v, old_v)):
+                assert torch.equal(new.view(b, budget, heads, 64)[i, :len(want), h], old.view(b, rows, heads, 64)[i, at, h])
+            assert torch.equal(new_mass[i, h, :len(want)].cpu(), mass[i, h, want])
+
+
+@gpu
 def test_kv_binding_refuses_what_does_not_fit():
     c = Case([20, 20], 2, 64, 16, 64, F16)
     k = torch.zeros(2, 128, dtype=F16, device="cuda")
