@@ -563,6 +563,68 @@ def test_captured_decode_step_follows_growing_lengths():
 
 
 @gpu
+@pytest.mark.parametrize("lens", [[0], [1], [130], [700, 0, 33], [0, 0, 0, 0, 5000]])
+def test_attention_of_short_sequences_under_a_large_capacity(lens):
+    # the work is laid out for max_len: most CTAs have none, and a workspace of
+    # junk and page numbers past a sequence's last page are never read
+    b, heads, dim, page, width = len(lens), 2, 128, 64, 4096
+    c = Case(lens, heads, dim, page, 128, F16)
+    table = torch.full((b, width), -7, dtype=torch.int32, device="cuda")
+    table[:, :c.width] = c.table
+    q = rnd((2 * b, 8 * dim), 3, F16)
+    want, p, bound, p_bound = R.attention(q.view(b, 2, 8, dim), c.k, c.v, lens, 2, dim ** -0.5)
+    for max_len in (width * page, max(max(lens), 1)):
+        for tracked in (False, True):
+            mass = torch.zeros(b, heads, width * page, device="cuda") if tracked else None
+            need = Q.stagq_kv_attention_workspace(c.cache, b, max_len, 8, 2, tracked)
+            ws = torch.full((need + 256,), 0xFF, dtype=torch.uint8, device="cuda")
+            out = torch.full((2 * b, 8 * dim), 3.0, dtype=F16, device="cuda")
+            for _ in range(2):  # and a workspace that holds the last call's sums
+                Q.stagq_kv_attention(c.cache, q.cuda(), table, c.lens, out, n_new=2, mass=mass, max_len=max_len, workspace=ws)
+                Q.stagq_ops_check(0)
+                assert_rounded(out.view(want.shape), want, F16, bound[..., None], f"{max_len} {tracked}")
+            assert (ws[need:] == 0xFF).all()
+            if tracked:
+                n = p.shape[2]
+                assert ((mass[:, :, :n].double().cpu() - 2 * p).abs() <= 2 * p_bound + 2.0 ** -22 * p).all()
+                assert not mass[:, :, n:].any()
+
+
+@gpu
+def test_calls_on_two_streams_at_once():
+    c = Case([900, 31], 2, 128, 32, 64, BF16)
+    jobs = []
+    for i in range(2):
+        a, xs, b, ws, _ = _i8(300, 2048, 700, 40 + i)
+        x = rnd((300, 2048), 60 + i, BF16).cuda()
+        q = rnd((2, 8 * 128), 50 + i, BF16).cuda()
+
+        def job(x=x, b=b, ws=ws, q=q, stream=None):
+            n, w = x.shape[0], b.shape[1]
+            xq, xs = torch.empty(n, w, dtype=torch.int8, device="cuda"), torch.empty(n, device="cuda")
+            y, small = torch.empty(n, 700, device="cuda"), torch.empty(9, 700, device="cuda")
+            out, mass = torch.empty_like(q), torch.zeros(2, 2, c.width * 32, device="cuda")
+            Q.stagq_quantize_i8(x, xq, xs)
+            Q.stagq_gemm_i8(xq, xs, b, ws, 2048, y)
+            Q.stagq_gemm_i8(xq[:9], xs[:9], b, ws, 2048, small)
+            Q.stagq_kv_attention(c.cache, q, c.table, c.lens, out, mass=mass)
+            return y, small, out, mass
+
+        jobs.append((job, [t.clone() for t in job()], torch.cuda.Stream()))
+    torch.cuda.synchronize()
+    got = []
+    for _ in range(20):
+        for job, _, stream in jobs:
+            with torch.cuda.stream(stream):
+                got.append(job())
+    torch.cuda.synchronize()
+    for i, outs in enumerate(got):
+        for have, want in zip(outs, jobs[i % 2][1]):
+            assert torch.equal(have, want), i
+    Q.stagq_ops_check(0)
+
+
+@gpu
 def test_attention_reads_offsets_beyond_32_bits():
     # a pool of more than 4 GiB whose used pages lie at its end
     heads, dim, page = 8, 128, 64
