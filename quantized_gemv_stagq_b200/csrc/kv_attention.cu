@@ -923,7 +923,8 @@ __global__ void __launch_bounds__(512) kv_join_kernel(const __grid_constant__ Kv
     for (int r = 0; r < 4; ++r) {
       const float lse = s_lse[min(r0 + r, a.rows - 1)];
 #pragma unroll
-      for (int i = 0; i < PER; ++i) sum[i] += ex2(s[r][i] - lse);
+      for (int i = 0; i < PER; ++i)  // a token that the row does not see stays out of a row whose lse is NaN
+        sum[i] += s[r][i] == -INFINITY ? 0.0f : ex2(s[r][i] - lse);
     }
   }
 #pragma unroll
