@@ -506,6 +506,9 @@ int64_t stagq_kv_attention_workspace(const stagq_kv_cache* cache, int32_t batch,
  * to positions 0, 1, ... of the pages in `fresh`. Those must be none of the
  * pages that `table` lists; the old pages are only read, so other sequences may
  * share them. Sequences of at most `budget` tokens are copied whole.
+ * A kept token whose page number in `table` is not in the pool becomes a row of
+ * zeros, as stagq_kv_read gives it, and is reported (STAGQ_EFORMAT); one whose
+ * place in `fresh` is not in the pool is reported and written nowhere.
  *   mass      fp32 [batch, heads, >= max_len]
  *   kept      device int32 [batch, heads, budget]: the old position of each
  *             kept token, -1 past the last

@@ -548,9 +548,16 @@ __global__ void __launch_bounds__(256) kv_move_kernel(const __grid_constant__ Kv
     if (from[k] < 0) continue;
     m[k] = a.mass[b * a.mass_stride_b + h * a.mass_stride_h + from[k]];
     const uint8_t* src = kv_block(kv, b, from[k], h);
-    dst[k] = src ? kv_block(a.dst, b, i0 + 64 * k, h) : nullptr;
-    if (!dst[k]) {
-      if (t == 0) atomicOr(&g_status, kOpsBadPage);
+    dst[k] = kv_block(a.dst, b, i0 + 64 * k, h);
+    if ((!src || !dst[k]) && t == 0) atomicOr(&g_status, kOpsBadPage);
+    if (!dst[k]) continue;
+    if (!src) {  // the row is listed as kept: zeros, as a read of it gives, and not what the fresh page held
+#pragma unroll
+      for (int which = 0; which < 2; ++which) {
+#pragma unroll
+        for (int w = 0; w < W; ++w) codes[k][which][w] = 0u;
+        meta[k][which] = 0u;
+      }
       continue;
     }
     const int slot = from[k] & (kv.page - 1);

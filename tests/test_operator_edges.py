@@ -45,3 +45,38 @@ def test_a_query_that_is_not_finite_spoils_no_mass_that_it_does_not_see(tokens, 
         assert ((got[b, h, lo:n] - p[b, h, lo:n]).abs() <= p_bound[b, h, lo:n] + 2.0 ** -24 * p[b, h, lo:n]).all(), (b, h)
         assert not got[b, h, n:].any()
     Q.stagq_ops_check(0)
+
+
+# ----------------------------------------------------------------- eviction
+
+@gpu
+@pytest.mark.parametrize("dim,group,budget", [(64, 32, 40), (128, 128, 24)])
+def test_evict_of_a_token_on_a_bad_page_leaves_zeros_and_not_the_fresh_pages_bytes(dim, group, budget):
+    heads, page, n = 2, 16, 40
+    c = Case([n, 33], heads, dim, page, group, F16, spare=6)  # what no call wrote is 0xFF: NaN pairs
+    fresh = c.unused.reshape(2, 3).cuda()
+    mass = torch.rand(2, heads, c.width * page, generator=torch.Generator().manual_seed(1))
+    mass[0, :, 16:32] += 1  # the bad page's tokens are kept
+    table = c.table.clone()
+    kept, new_lens = torch.empty(2, heads, budget, dtype=torch.int32, device="cuda"), torch.empty(2, dtype=torch.int32, device="cuda")
+    new_mass = torch.empty(2, heads, budget, device="cuda")
+    k, v = (torch.empty(2 * budget, heads * dim, device="cuda") for _ in range(2))
+    for number in (-1, c.pool.shape[0]):
+        c.pool[c.unused.long().cuda()] = 0xFF
+        table[0, 1] = number
+        Q.stagq_kv_evict(c.cache, table, c.lens, mass.cuda(), fresh, budget, 3, kept, new_lens, new_mass)
+        with pytest.raises(Q.StagqError) as e:
+            Q.stagq_ops_check(0)
+        assert e.value.status == EFORMAT
+        Q.stagq_kv_read(c.cache, fresh, new_lens, k, v, budget)
+        Q.stagq_ops_check(0)
+        for b, m in enumerate((n, 33)):
+            for h in range(heads):
+                want = R.keep(mass[b, h].numpy(), m, budget, 3)
+                assert kept[b, h].tolist() == want + [-1] * (budget - len(want))
+                assert torch.equal(new_mass[b, h, :len(want)].cpu(), mass[b, h, want])
+                for got, values in ((k, c.k), (v, c.v)):
+                    x = values[b, want, h].clone()
+                    if b == 0:
+                        x[[i for i, t in enumerate(want) if 16 <= t < 32]] = 0
+                    assert_rounded(got.view(2, budget, heads, dim)[b, :len(want), h], x, F32)
