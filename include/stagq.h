@@ -515,6 +515,8 @@ int64_t stagq_kv_attention_workspace(const stagq_kv_cache* cache, int32_t batch,
  *   new_lens  device int32 [batch]: min(lens[b], budget)
  *   new_mass  fp32 [batch, heads, new_cap] (budget <= new_cap): the kept
  *             tokens' masses, then zeros
+ * Nothing is done in place: new_lens = lens, new_mass = mass and fresh = table
+ * are refused.
  * lens, max_len: as stagq_kv_attention. Errors: STAGQ_EINVAL, STAGQ_ECUDA.
  */
 int stagq_kv_evict(const stagq_kv_cache* cache, const stagq_kv_table* table, const int32_t* lens, int32_t max_len,

@@ -747,7 +747,8 @@ def stagq_kv_evict(cache: KVCache, table, lens, mass, fresh, budget: int, recent
     """Thins every sequence out to `budget` tokens per KV head: its last
     `recent` ones and those of the largest mass, copied in their order to the
     pages of `fresh` (none of table's). kept int32 [batch, heads, budget];
-    new_lens int32 [batch]; new_mass fp32 [batch, heads, >= budget]."""
+    new_lens int32 [batch]; new_mass fp32 [batch, heads, >= budget]. Not in
+    place: new_lens, new_mass and fresh are not lens, mass and table."""
     t, f = cache._table(table), cache._table(fresh, "fresh")
     dev = cache.device
     if f.batch != t.batch:

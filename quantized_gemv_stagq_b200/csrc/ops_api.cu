@@ -324,6 +324,8 @@ extern "C" int stagq_kv_evict(const stagq_kv_cache* c, const stagq_kv_table* t, 
     return bad("mass rows overlap");
   const int64_t heads = static_cast<int64_t>(t->batch) * c->heads;
   if (heads * ((static_cast<int64_t>(new_cap) + 63) / 64) > INT_MAX) return bad("too many rows for one call");
+  // heads read lens, masses and pages while others already write theirs
+  if (new_lens == lens || new_mass == mass || fresh->pages == t->pages) return bad("new_lens, new_mass and fresh must not be lens, mass and the table");
   OpsDevice guard(c->device);
   if (!guard.ok) return fail(STAGQ_ECUDA, "cudaSetDevice failed");
   KvEvictArgs a{};

@@ -80,3 +80,30 @@ def test_evict_of_a_token_on_a_bad_page_leaves_zeros_and_not_the_fresh_pages_byt
                     if b == 0:
                         x[[i for i, t in enumerate(want) if 16 <= t < 32]] = 0
                     assert_rounded(got.view(2, budget, heads, dim)[b, :len(want), h], x, F32)
+
+
+def _evict_in_c(**kw):
+    """stagq_kv_evict of 2 sequences on pointers that are never read, as every call here is refused."""
+    f = dict(heads=2, page=16, table=8192, fresh=16384, batch=2, width=4, lens=1, max_len=64, mass=2, mb=128, mh=64, budget=8,
+             recent=2, kept=3, new_lens=4, new_mass=5, nb=128, nh=64, cap=64)
+    f.update(kw)
+    cache = Q._KvCache(4096, 4, f["heads"], 128, f["page"], 128, 0, 0)
+    t, fresh = (Q._KvTable(f[n], f["width"], f["batch"], f["width"]) for n in ("table", "fresh"))
+    p = {n: ctypes.c_void_p(4096 * f[n]) for n in ("lens", "mass", "kept", "new_lens", "new_mass")}
+    r = ctypes.byref
+    return Q.lib().stagq_kv_evict(r(cache), r(t), p["lens"], f["max_len"], p["mass"], f["mb"], f["mh"], f["budget"], f["recent"],
+                                  r(fresh), p["kept"], p["new_lens"], p["new_mass"], f["nb"], f["nh"], f["cap"], None)
+
+
+@pytest.mark.parametrize("kw", [dict(new_lens=1), dict(new_mass=2), dict(fresh=8192)])
+def test_evict_refuses_to_work_in_place(kw):
+    assert _evict_in_c(**kw) == EINVAL
+    assert "must not be" in Q.lib().stagq_last_error().decode()
+
+
+@pytest.mark.parametrize("kw", [dict(lens=0), dict(mass=0), dict(kept=0), dict(new_lens=0), dict(new_mass=0), dict(fresh=0), dict(table=0),
+                                dict(max_len=0), dict(max_len=65), dict(budget=0), dict(budget=65), dict(recent=-1), dict(recent=9),
+                                dict(cap=7), dict(mh=63), dict(nh=63), dict(mb=127), dict(nb=127), dict(page=8), dict(batch=0)])
+def test_evict_refuses_what_does_not_fit(kw):
+    assert _evict_in_c(**kw) == EINVAL
+    assert "must not be" not in Q.lib().stagq_last_error().decode()  # for its own reason
