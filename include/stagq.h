@@ -513,8 +513,8 @@ int64_t stagq_kv_attention_workspace(const stagq_kv_cache* cache, int32_t batch,
  *   kept      device int32 [batch, heads, budget]: the old position of each
  *             kept token, -1 past the last
  *   new_lens  device int32 [batch]: min(lens[b], budget)
- *   new_mass  fp32 [batch, heads, new_cap] (budget <= new_cap): the kept
- *             tokens' masses, then zeros
+ *   new_mass  fp32 [batch, heads, new_cap] (budget <= new_cap <=
+ *             STAGQ_KV_MAX_TOKENS): the kept tokens' masses, then zeros
  * Nothing is done in place: new_lens = lens, new_mass = mass and fresh = table
  * are refused.
  * lens, max_len: as stagq_kv_attention. Errors: STAGQ_EINVAL, STAGQ_ECUDA.

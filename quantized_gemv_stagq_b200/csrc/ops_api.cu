@@ -318,12 +318,13 @@ extern "C" int stagq_kv_evict(const stagq_kv_cache* c, const stagq_kv_table* t, 
   if (budget < 1 || budget > static_cast<int64_t>(fresh->width) * c->page) return bad("budget outside 1..the fresh table's tokens");
   if (recent < 0 || recent > budget) return bad("recent outside 0..budget");
   if (new_cap < budget) return bad("new_mass holds fewer than budget entries");
+  if (new_cap > STAGQ_KV_MAX_TOKENS) return bad("new_cap exceeds STAGQ_KV_MAX_TOKENS");
   if (mass_stride_h < max_len || new_mass_stride_h < new_cap) return bad("mass rows overlap");
   if (t->batch > 1 && (mass_stride_b < mass_stride_h * (c->heads - 1) + max_len ||
                        new_mass_stride_b < new_mass_stride_h * (c->heads - 1) + new_cap))
     return bad("mass rows overlap");
   const int64_t heads = static_cast<int64_t>(t->batch) * c->heads;
-  if (heads * ((static_cast<int64_t>(new_cap) + 63) / 64) > INT_MAX) return bad("too many rows for one call");
+  if (heads > INT_MAX || heads * ((static_cast<int64_t>(new_cap) + 63) / 64) > INT_MAX) return bad("too many rows for one call");
   // heads read lens, masses and pages while others already write theirs
   if (new_lens == lens || new_mass == mass || fresh->pages == t->pages) return bad("new_lens, new_mass and fresh must not be lens, mass and the table");
   OpsDevice guard(c->device);

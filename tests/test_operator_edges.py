@@ -107,3 +107,11 @@ def test_evict_refuses_to_work_in_place(kw):
 def test_evict_refuses_what_does_not_fit(kw):
     assert _evict_in_c(**kw) == EINVAL
     assert "must not be" not in Q.lib().stagq_last_error().decode()  # for its own reason
+
+
+@pytest.mark.parametrize("kw", [dict(heads=1, batch=1, cap=2 ** 31 - 1, nh=2 ** 31, nb=2 ** 31),  # the kernel rounds new_cap up
+                                dict(heads=1, batch=1, cap=2 ** 30 + 1, nh=2 ** 31, nb=2 ** 31),
+                                # heads times chunks of new_cap is 2^67 and wraps to a negative number
+                                dict(heads=4096, batch=2 ** 31 - 1, cap=2 ** 30, nh=2 ** 30, nb=2 ** 42, mb=2 ** 18)])
+def test_evict_refuses_sizes_that_its_indices_do_not_hold(kw):
+    assert _evict_in_c(**kw) == EINVAL
