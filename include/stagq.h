@@ -546,6 +546,17 @@ int stagq_ops_check(int device);
 int stagq_debug_stall(stagq_handle h, uint32_t stall_ns);
 
 /*
+ * The same for the operators beside the GEMV: while stall_ns != 0, every
+ * stagq_gemm_i8 and stagq_kv_attention launched on `device` (captured ones
+ * keep the value of their capture) has waits of at most stall_ns on a barrier
+ * that nothing completes, in one warp or another of each CTA. The kernel gives
+ * up: the copies and MMAs in flight end, its output is undefined, and the next
+ * stagq_ops_check returns STAGQ_ETIMEOUT. 0 turns the hook off. Errors:
+ * STAGQ_EINVAL.
+ */
+int stagq_debug_stall_ops(int device, uint32_t stall_ns);
+
+/*
  * Where the handle's side record lives on the device: the loader re-lays the
  * CSR record (Eq. 4) per CTA for each kernel's grid.
  *   General kernel (grid CTAs, stride bytes each): CTA b owns rows

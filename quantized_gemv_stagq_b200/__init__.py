@@ -113,6 +113,7 @@ _SIGNATURES = {
     "stagq_kv_evict": (ctypes.c_int, [_CACHE_P, _TABLE_P, _c_p, _i32, _c_p, _i64, _i64, _i32, _i32, _TABLE_P, _c_p, _c_p,
                                       _c_p, _i64, _i64, _i32, _c_p]),
     "stagq_ops_check": (ctypes.c_int, [ctypes.c_int]),
+    "stagq_debug_stall_ops": (ctypes.c_int, [ctypes.c_int, _u32]),
     "stagq_free": (None, [_c_p]),
     "stagq_strerror": (ctypes.c_char_p, [ctypes.c_int]),
     "stagq_last_error": (ctypes.c_char_p, []),
@@ -772,3 +773,8 @@ def stagq_ops_check(device: int = 0) -> None:
     """Waits for the device and raises on what the operators' kernels noted: a
     page number, position or length out of bounds, or a wait that ran out."""
     _check(lib().stagq_ops_check(device), "stagq_ops_check")
+
+
+def stagq_debug_stall_ops(device: int, stall_ns: int) -> None:
+    """Test hook: the operators launched on the device give up a wait of stall_ns; 0 turns it off."""
+    _check(lib().stagq_debug_stall_ops(device, stall_ns), "stagq_debug_stall_ops")

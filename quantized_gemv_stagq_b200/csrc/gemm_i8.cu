@@ -211,6 +211,10 @@ __device__ __forceinline__ void mma_commit_pair(uint32_t bar) {
       "h"(static_cast<uint16_t>(3))
       : "memory");
 }
+// To the first CTA alone.
+__device__ __forceinline__ void mma_commit_pair_here(uint32_t bar) {
+  asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
+}
 __device__ __forceinline__ void mbar_arrive_cluster(uint32_t bar) {
   asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
@@ -302,10 +306,16 @@ __global__ void __launch_bounds__(kGemmThreads) gemm_i8_kernel(const __grid_cons
     atomicOr(&g_status, kOpsTimeout);
   };
 
+  // Test hook: one of the roles waits for what nothing completes, which one by the block's number.
+  auto stalled = [&](int role) {
+    return a.stall_ns && static_cast<int>(blockIdx.x % 3) == role && !kernels::mbar_wait(drained, 0, a.stall_ns);
+  };
+  uint32_t issued = 0;  // K blocks that this thread has asked for
+
   if (warp == 0) {
     if (lane == 0) {
       uint32_t it = 0;
-      bool ok = true;
+      bool ok = !stalled(0);
       for (int w = first; w < n_work && ok; w += step) {
         const int m0 = (w % a.m_tiles) * kBM, n0 = (w / a.m_tiles) * BN;
         for (int k = k0; k < k1; ++k, ++it) {
@@ -320,18 +330,14 @@ __global__ void __launch_bounds__(kGemmThreads) gemm_i8_kernel(const __grid_cons
           tma_load_2d(dst + kBM * kBK, &xmap, k * kBK, n0, full(s));
         }
       }
-      if (!ok) {
-        give_up();
-        // let the copies in flight land before the CTA's shared memory goes
-        for (uint32_t j = it < STAGES ? 0 : it - STAGES; j < it; ++j)
-          kernels::mbar_wait(full(j % STAGES), (j / STAGES) & 1, kWaitLimitNs);
-      }
+      if (!ok) give_up();
+      issued = it;
     }
   } else if (warp == 1) {
     if (lane == 0) {
       constexpr uint32_t idesc = instr_desc(BN, kBM);
       uint32_t it = 0, tile = 0;
-      bool ok = true;
+      bool ok = !stalled(1);
       for (int w = first; w < n_work && ok; w += step, ++tile) {
         const int buf = tile % ACC;
         if (!mbar_wait_unless(acc_empty(buf), ((tile / ACC) & 1) ^ 1, kWaitLimitNs, stop)) {
@@ -354,17 +360,14 @@ __global__ void __launch_bounds__(kGemmThreads) gemm_i8_kernel(const __grid_cons
         }
         if (ok) mma_commit(acc_full(buf));
       }
-      if (!ok) {
-        give_up();
-        mma_commit(drained);  // no MMA may still read the ring or write TMEM when the CTA goes
-        kernels::mbar_wait(drained, 0, kWaitLimitNs);
-      }
+      if (!ok) give_up();
     }
   } else {
     const int quarter = warp & 3;  // the TMEM lanes that this warp may read
     const int row = quarter * 32 + lane;
     uint32_t tile = 0;
-    bool ok = true;
+    bool ok = !__any_sync(kFull, stalled(2));
+    if (!ok && lane == 0) give_up();
     for (int w = first; w < n_work && ok; w += step, ++tile) {
       const int o = (w % a.m_tiles) * kBM + row, n0 = (w / a.m_tiles) * BN;
       const int cols = min(BN, a.n - n0);
@@ -433,6 +436,20 @@ __global__ void __launch_bounds__(kGemmThreads) gemm_i8_kernel(const __grid_cons
   asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
   __syncthreads();
   asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+  if (*stop) {
+    // A wait ran out, in whichever warp: the copies and MMAs in flight end
+    // before shared memory and TMEM go. (Else the epilogue has seen the MMAs
+    // complete, and they have consumed every copy.)
+    if (threadIdx.x == 0)
+      for (uint32_t j = issued < STAGES ? 0 : issued - STAGES; j < issued; ++j)
+        kernels::mbar_wait(full(j % STAGES), (j / STAGES) & 1, kWaitLimitNs);
+    if (threadIdx.x == 32) {
+      mma_commit(drained);
+      kernels::mbar_wait(drained, 0, kWaitLimitNs);
+    }
+    __syncthreads();
+    asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+  }
   if (warp == 1)
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(tmem_cols(BN)));
 }
@@ -457,6 +474,16 @@ __device__ __forceinline__ uint32_t in_first_cta(uint32_t addr) {
   uint32_t r;
   asm volatile("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(r) : "r"(addr));
   return r;
+}
+
+__device__ __forceinline__ void store_peer(uint32_t addr, uint32_t rank, uint32_t v) {
+  uint32_t peer;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(peer) : "r"(addr), "r"(rank));
+  asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(peer), "r"(v) : "memory");
+}
+// Counts bytes as arrived that no copy will bring.
+__device__ __forceinline__ void mbar_complete_tx(uint32_t bar, uint32_t bytes) {
+  asm volatile("mbarrier.complete_tx.relaxed.cta.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
 }
 
 constexpr int kPairThreads = 320;  // TMA warp, MMA warp, eight epilogue warps
@@ -516,6 +543,7 @@ __global__ void __launch_bounds__(kPairThreads) gemm_i8_pair_kernel(const __grid
   extern __shared__ uint8_t smem_raw[];
   __shared__ uint32_t s_tmem;
   __shared__ uint32_t s_stop;
+  __shared__ uint32_t s_issued[2];                  // the first CTA's: K blocks that each CTA has asked for
   __shared__ __align__(16) float s_ws[8][BN / 2];  // scales of an epilogue warp's channels
   __shared__ TurnBuffer s_turn[8];
   const uint32_t ring = (smem_addr(smem_raw) + 1023u) & ~1023u;
@@ -558,16 +586,21 @@ __global__ void __launch_bounds__(kPairThreads) gemm_i8_pair_kernel(const __grid
   grid_dependency_wait();
 
   const int n_work = a.m_tiles * a.n_tiles, first = blockIdx.x >> 1, step = gridDim.x >> 1;
-  auto give_up = [&]() {
+  auto give_up = [&]() {  // both CTAs stop: neither gets on without the other
     s_stop = 1;
     __threadfence_block();
+    store_peer(smem_addr(&s_stop), rank ^ 1, 1);
     atomicOr(&g_status, kOpsTimeout);
+  };
+  // Test hook: one of the roles waits for what nothing completes, which one by the pair's number.
+  auto stalled = [&](int role) {
+    return a.stall_ns && first % 4 == role && !kernels::mbar_wait(drained, 0, a.stall_ns);
   };
 
   if (warp == 0) {
     if (lane == 0) {
       uint32_t it = 0;
-      bool ok = true;
+      bool ok = !stalled(rank);
       for (int w = first; w < n_work && ok; w += step) {
         const int m0 = (w % a.m_tiles) * 2 * kBM + rank * kBM, c0 = (w / a.m_tiles) * BN + rank * (BN / 2);
         for (int k = 0; k < a.kblocks; ++k, ++it) {
@@ -582,25 +615,14 @@ __global__ void __launch_bounds__(kPairThreads) gemm_i8_pair_kernel(const __grid
           tma_load_2d_pair(dst + kBM * kBK, &wmap, k * kBK, c0, bar);
         }
       }
-      if (!ok) {
-        give_up();
-        // the copies in flight land before either CTA's shared memory goes: the
-        // first CTA sees both CTAs', the second can only give its own a millisecond
-        if (rank == 0) {
-          for (uint32_t j = it < STAGES ? 0 : it - STAGES; j < it; ++j)
-            kernels::mbar_wait(full(j % STAGES), (j / STAGES) & 1, kWaitLimitNs);
-        } else {
-          const uint64_t t0 = kernels::global_timer();
-          while (kernels::global_timer() - t0 < 1000000) {
-          }
-        }
-      }
+      if (!ok) give_up();
+      store_peer(smem_addr(&s_issued[rank]), 0, it);
     }
   } else if (warp == 1) {
     if (rank == 0 && lane == 0) {
       constexpr uint32_t idesc = instr_desc(BN, 2 * kBM);
       uint32_t it = 0, tile = 0;
-      bool ok = true;
+      bool ok = !stalled(2);
       for (int w = first; w < n_work && ok; w += step, ++tile) {
         const int buf = tile % ACC;
         if (!mbar_wait_unless(acc_empty(buf), ((tile / ACC) & 1) ^ 1, kWaitLimitNs, stop)) {
@@ -622,17 +644,15 @@ __global__ void __launch_bounds__(kPairThreads) gemm_i8_pair_kernel(const __grid
         }
         if (ok) mma_commit_pair(acc_full(buf));
       }
-      if (!ok) {
-        give_up();
-        mma_commit_pair(drained);  // no MMA may still read the rings or write TMEM when the CTAs go
-        kernels::mbar_wait(drained, 0, kWaitLimitNs);
-      }
+      if (!ok) give_up();
     }
   } else {
     const int quarter = warp & 3, half = (warp - 2) >> 2;
     float* scales = s_ws[warp - 2];
     uint32_t tile = 0;
-    for (int w = first; w < n_work; w += step, ++tile) {
+    bool ok = !__any_sync(kFull, stalled(3));
+    if (!ok && lane == 0) give_up();
+    for (int w = first; w < n_work && ok; w += step, ++tile) {
       const int tok = (w % a.m_tiles) * 2 * kBM + rank * kBM + quarter * 32 + lane;
       const int o0 = (w / a.m_tiles) * BN + half * (BN / 2);
       const int buf = tile % ACC;
@@ -640,7 +660,7 @@ __global__ void __launch_bounds__(kPairThreads) gemm_i8_pair_kernel(const __grid
 #pragma unroll
       for (int i = lane; i < BN / 2; i += 32) scales[i] = o0 + i < a.out ? __ldg(a.ws + o0 + i) : 0.0f;
       __syncwarp();
-      bool ok = mbar_wait_unless(acc_full(buf), (tile / ACC) & 1, kWaitLimitNs, stop);
+      ok = mbar_wait_unless(acc_full(buf), (tile / ACC) & 1, kWaitLimitNs, stop);
       ok = __all_sync(kFull, ok);
       if (!ok) {
         if (lane == 0) give_up();
@@ -663,6 +683,29 @@ __global__ void __launch_bounds__(kPairThreads) gemm_i8_pair_kernel(const __grid
   asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
   __syncthreads();
   cluster_sync_all();  // neither CTA's memory goes while the other's MMAs or copies use it
+  if (*stop) {
+    // A wait ran out, in whichever warp of the two CTAs (both see it: it was
+    // noted before the barrier above). The MMAs and both CTAs' copies in flight
+    // end before memory goes. The copies complete on the first CTA's barriers,
+    // which expect both CTAs' bytes of a block that it asked for; a block that
+    // only one of the two asked for is evened out here.
+    if (rank == 0 && threadIdx.x == 0) {
+      const uint32_t n0 = s_issued[0], n1 = s_issued[1], n = max(n0, n1);
+      for (uint32_t j = n < STAGES ? 0 : n - STAGES; j < n; ++j) {
+        if (j >= n0)
+          mbar_arrive_expect_tx(full(j % STAGES), STAGE);
+        else if (j >= n1)
+          mbar_complete_tx(full(j % STAGES), STAGE);
+        kernels::mbar_wait(full(j % STAGES), (j / STAGES) & 1, kWaitLimitNs);
+      }
+    }
+    if (rank == 0 && threadIdx.x == 32) {
+      mma_commit_pair_here(drained);
+      kernels::mbar_wait(drained, 0, kWaitLimitNs);
+    }
+    __syncthreads();
+    cluster_sync_all();
+  }
   asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
   if (warp == 1) asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(2 * BN));
 }

@@ -25,6 +25,7 @@ struct GemmI8Args {
   int32_t m_tiles, n_tiles, split;
   int32_t wide;                      // every row of y is aligned to 16 bytes
   int32_t y_f32, y_bf16;
+  uint32_t stall_ns;                 // test hook: a wait of this length that runs out
 };
 
 // The tile and split that plan_gemm_i8 chose.

@@ -217,7 +217,7 @@ __global__ void __launch_bounds__(kWarps * 32, resident_ctas(NT)) kv_attention_k
   static_assert(kStages * L::kBytes >= 2 * ROWS * D * 4, "the warps' sums take the rings' place");
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ float s_m[kWarps][ROWS], s_l[kWarps][ROWS];
-  __shared__ __align__(8) uint64_t s_full[kWarps][kStages];
+  __shared__ __align__(8) uint64_t s_full[kWarps][kStages + 1];  // the last: nothing completes it (test hook)
   __shared__ uint32_t s_ok[kWarps][kStages];  // by lane: whether its piece's page is in the pool
   __shared__ float s_top[ROWS], s_den[ROWS];  // of the CTA, for its cluster
   __shared__ __align__(16) uint16_t s_q[ROWS][D];
@@ -232,7 +232,7 @@ __global__ void __launch_bounds__(kWarps * 32, resident_ctas(NT)) kv_attention_k
 
   uint8_t* ring = smem + warp * (kStages * L::kBytes);
   const uint32_t ring_addr = kernels::smem_addr(ring), full_addr = kernels::smem_addr(&s_full[warp][0]);
-  if (lane < kStages) kernels::mbar_init(full_addr + 8 * lane, 1);
+  if (lane <= kStages) kernels::mbar_init(full_addr + 8 * lane, 1);
   kernels::fence_barrier_init();
   __syncthreads();
   uint32_t filled = 0, used = 0;  // tiles that this warp has asked for, and waited for
@@ -436,6 +436,15 @@ __global__ void __launch_bounds__(kWarps * 32, resident_ctas(NT)) kv_attention_k
   asm volatile("mov.b32 %0, 0x64006400;" : "=r"(exponent));
   const uint32_t rest_mask = t < 2 ? 0u : 0xFFFFE000u;
   const int tau_g = tau(g), tau_v = tau(2 * t), tau_w = tau(2 * t + 1);
+  auto give_up = [&]() {
+    dead = true;
+    if (lane == 0) atomicOr(&g_status, kOpsTimeout);
+    for (; used < filled; ++used)  // the copies in flight land before the sums take their place
+      kernels::mbar_wait(full_addr + 8 * (used % kStages), (used / kStages) & 1, kWaitLimitNs);
+  };
+  if (__builtin_expect(a.stall_ns != 0, 0) && tile < tile_end && !dead &&  // test hook
+      !__all_sync(kFull, kernels::mbar_wait(full_addr + 8 * kStages, 0, a.stall_ns)))
+    give_up();
   for (; tile < tile_end && !dead; tile += kWarps) {
     if (ahead < tile_end) {
       ask(ahead, pid);
@@ -443,14 +452,11 @@ __global__ void __launch_bounds__(kWarps * 32, resident_ctas(NT)) kv_attention_k
       if (ahead < tile_end) pid = page_of(ahead);
     }
     const int stage = used % kStages;
-    dead = !__all_sync(kFull, kernels::mbar_wait(full_addr + 8 * stage, (used / kStages) & 1, kWaitLimitNs));
-    ++used;
-    if (dead) {
-      if (lane == 0) atomicOr(&g_status, kOpsTimeout);
-      for (; used < filled; ++used)  // the copies in flight land before the CTA goes
-        kernels::mbar_wait(full_addr + 8 * (used % kStages), (used / kStages) & 1, kWaitLimitNs);
+    if (!__all_sync(kFull, kernels::mbar_wait(full_addr + 8 * stage, (used / kStages) & 1, kWaitLimitNs))) {
+      give_up();
       break;
     }
+    ++used;
     const uint8_t* x = ring + stage * L::kBytes;
     const uint32_t okm = s_ok[warp][stage];
     const int tok0 = tile * kTile + tau_g;  // this lane's tokens: tok0 + 8 n

@@ -68,6 +68,7 @@ struct KvAttnArgs {
   int32_t batch, q_heads, per, n_new, rows, rows_pad, row_blocks, ctas, max_len, vec_out;
   int32_t cluster;         // CTAs per unit, or 0: the even split
   float scale_log2;        // softmax scale times log2(e)
+  uint32_t stall_ns;       // test hook: a wait of this length that runs out
 };
 
 struct KvEvictArgs {

@@ -1,5 +1,6 @@
 // C ABI of the operators beside the GEMV: argument checks and launches. See
 // include/stagq.h for the contract of each function.
+#include <atomic>
 #include <climits>
 #include <cmath>
 #include <string>
@@ -38,6 +39,8 @@ int sm_count(int device) {
   }
   return known[device];
 }
+
+std::atomic<uint32_t> g_stall_ns[kMaxDevices];  // stagq_debug_stall_ops
 
 // Error text, or null.
 const char* cache_error(const stagq_kv_cache* c) {
@@ -158,6 +161,7 @@ extern "C" int stagq_gemm_i8(const int8_t* xq, const float* xscale, int32_t n, c
   a.out = out;
   a.y_f32 = (flags & STAGQ_Y_F32) ? 1 : 0;
   a.y_bf16 = (flags & STAGQ_BF16) ? 1 : 0;
+  a.stall_ns = g_stall_ns[device];
   bool encode_failed = false;
   const GemmI8Plan p = plan_gemm_i8(n, out, static_cast<int>(ld / STAGQ_I8_ROW_MULTIPLE), sms);
   const cudaError_t e = launch_gemm_i8(a, p, xq, wq, static_cast<int>(ld), static_cast<cudaStream_t>(cuda_stream), &encode_failed);
@@ -301,6 +305,7 @@ extern "C" int stagq_kv_attention(const stagq_kv_cache* c, const stagq_kv_table*
   a.max_len = max_len;
   a.vec_out = aligned(out, 8) && out_stride % 4 == 0;
   a.scale_log2 = scale * 1.4426950408889634f;
+  a.stall_ns = g_stall_ns[c->device];
   return launched(launch_kv_attention(a, p, static_cast<cudaStream_t>(cuda_stream)), "attention launch");
 }
 
@@ -366,5 +371,11 @@ extern "C" int stagq_ops_check(int device) {
   const uint32_t word = i8 | kv | at;
   if (word & kOpsTimeout) return fail(STAGQ_ETIMEOUT, "an operator's kernel gave up a bounded wait");
   if (word & kOpsBadPage) return fail(STAGQ_EFORMAT, "a page number, position or length lies outside the pool, the table or max_len");
+  return STAGQ_OK;
+}
+
+extern "C" int stagq_debug_stall_ops(int device, uint32_t stall_ns) {
+  if (device < 0 || device >= kMaxDevices) return bad("device index outside 0..63");
+  g_stall_ns[device] = stall_ns;
   return STAGQ_OK;
 }

@@ -115,3 +115,60 @@ def test_evict_refuses_what_does_not_fit(kw):
                                 dict(heads=4096, batch=2 ** 31 - 1, cap=2 ** 30, nh=2 ** 30, nb=2 ** 42, mb=2 ** 18)])
 def test_evict_refuses_sizes_that_its_indices_do_not_hold(kw):
     assert _evict_in_c(**kw) == EINVAL
+
+
+# ------------------------------------------------------------ waits that run out
+
+ETIMEOUT = 7
+
+
+def gave_up():
+    with pytest.raises(Q.StagqError) as e:
+        Q.stagq_ops_check(0)
+    Q.stagq_ops_check(0)  # reported once
+    return e.value.status == ETIMEOUT
+
+
+# tiles of 16, 32 and 64 tokens (K shared by clusters, and not), pairs on 128 and on 256 channels; few K blocks, and
+# many times the ring's
+STALLED = [(1, 4096, 300), (20, 512, 1000), (64, 32768, 640), (64, 256, 40000), (129, 640, 384), (1100, 2048, 1500), (2049, 4096, 2600)]
+
+
+@gpu
+@pytest.mark.parametrize("n,inp,out", STALLED)
+def test_gemm_i8_ends_when_a_wait_runs_out_and_works_again(n, inp, out):
+    g = torch.Generator(device="cuda").manual_seed(n)
+    a, b = (torch.randint(-127, 128, (r, inp), generator=g, device="cuda", dtype=torch.int8) for r in (n, out))
+    xs, ws = torch.ones(n, device="cuda"), torch.full((out,), 2.0 ** -10, device="cuda")
+    y = torch.empty(n, out, device="cuda")
+    for stall in (2000, 50000):
+        Q.stagq_debug_stall_ops(0, stall)
+        try:
+            Q.stagq_gemm_i8(a, xs, b, ws, inp, y)
+        finally:
+            Q.stagq_debug_stall_ops(0, 0)
+        assert gave_up()
+        y.fill_(float("nan"))
+        Q.stagq_gemm_i8(a, xs, b, ws, inp, y)
+        Q.stagq_ops_check(0)
+        assert torch.equal(y, (a.double() @ b.double().T).float() * 2.0 ** -10)  # |sum| < 2^29: one rounding on both sides
+
+
+@gpu
+@pytest.mark.parametrize("tracked", [False, True])
+@pytest.mark.parametrize("lens,heads,group,n_new", [([1], 1, 128, 1), ([777], 2, 128, 1), ([900, 0, 4000], 2, 32, 1), ([700, 33], 2, 64, 4)])
+def test_attention_ends_when_a_wait_runs_out_and_works_again(lens, heads, group, n_new, tracked):
+    c = Case(lens, heads, 128, 16, group, F16)
+    q = rnd((len(lens) * n_new, heads * 4 * 128), 5, F16).cuda()
+    for stall in (2000, 50000):
+        Q.stagq_debug_stall_ops(0, stall)
+        try:
+            c.attend(q, n_new, torch.zeros(len(lens), heads, c.width * 16, device="cuda") if tracked else None)
+        finally:
+            Q.stagq_debug_stall_ops(0, 0)
+        assert gave_up()
+        c.check(heads * 4, n_new, q=q.cpu(), tracked=tracked)
+
+
+def test_stall_hook_refuses_bad_devices():
+    assert Q.lib().stagq_debug_stall_ops(-1, 0) == EINVAL and Q.lib().stagq_debug_stall_ops(64, 0) == EINVAL
