@@ -520,6 +520,19 @@ __global__ void __launch_bounds__(kSelThreads) kv_select_kernel(const __grid_con
 // kMoveTokens tokens per thread load before any is stored. Bound by bytes: kept
 // rows read and written once.
 constexpr int kMoveTokens = 2;
+
+// The row of a kept token whose own page is not in the pool: zeros, as a read
+// of it gives, and not what the fresh page held. t: quarter of the row.
+template <int W>
+__device__ __noinline__ void zero_row(const KvView& kv, uint8_t* block, int pos, int t) {
+  if (!block) return;
+  const int slot = pos & (kv.page - 1), half = kv.dim >> 1, ng = kv.dim / kv.group;
+  for (int which = 0; which < 2; ++which, block += kv.block_bytes) {
+    for (int w = 0; w < W; ++w) reinterpret_cast<uint32_t*>(block + slot * half)[t * W + w] = 0u;
+    if (t < ng) reinterpret_cast<uint32_t*>(block + kv.page * half)[slot * ng + t] = 0u;
+  }
+}
+
 template <int D>
 __global__ void __launch_bounds__(256) kv_move_kernel(const __grid_constant__ KvEvictArgs a) {
   constexpr int W = D / 32;  // words of a quarter row
@@ -548,16 +561,10 @@ __global__ void __launch_bounds__(256) kv_move_kernel(const __grid_constant__ Kv
     if (from[k] < 0) continue;
     m[k] = a.mass[b * a.mass_stride_b + h * a.mass_stride_h + from[k]];
     const uint8_t* src = kv_block(kv, b, from[k], h);
-    dst[k] = kv_block(a.dst, b, i0 + 64 * k, h);
-    if ((!src || !dst[k]) && t == 0) atomicOr(&g_status, kOpsBadPage);
-    if (!dst[k]) continue;
-    if (!src) {  // the row is listed as kept: zeros, as a read of it gives, and not what the fresh page held
-#pragma unroll
-      for (int which = 0; which < 2; ++which) {
-#pragma unroll
-        for (int w = 0; w < W; ++w) codes[k][which][w] = 0u;
-        meta[k][which] = 0u;
-      }
+    dst[k] = src ? kv_block(a.dst, b, i0 + 64 * k, h) : nullptr;
+    if (!dst[k]) {
+      if (t == 0) atomicOr(&g_status, kOpsBadPage);
+      if (!src) zero_row<W>(a.dst, kv_block(a.dst, b, i0 + 64 * k, h), i0 + 64 * k, t);
       continue;
     }
     const int slot = from[k] & (kv.page - 1);
