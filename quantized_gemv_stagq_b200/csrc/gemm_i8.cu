@@ -380,7 +380,7 @@ __global__ void __launch_bounds__(kGemmThreads) gemm_i8_kernel(const __grid_cons
       }
       asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
       const uint32_t addr = tmem + buf * BN + (static_cast<uint32_t>(quarter * 32) << 16);
-      const float ws = o < a.out ? __ldg(a.ws + o) : 0.0f;
+      const float ws = o < a.out ? a.ws[o] : 0.0f;
       for (int c0 = 0; c0 < cols; c0 += 16) {
         int v[16];
         tmem_load16(addr + c0, v);
@@ -390,11 +390,12 @@ __global__ void __launch_bounds__(kGemmThreads) gemm_i8_kernel(const __grid_cons
 #pragma unroll
           for (int i = 0; i < 16; ++i) red[(c0 + i) * kBM + row] = v[i];
         } else if (o < a.out) {
+          float xs[16];  // all loads before the first store, which might be to the same place for all the compiler knows
+#pragma unroll
+          for (int i = 0; i < 16; ++i) xs[i] = c0 + i < cols ? a.xs[n0 + c0 + i] : 0.0f;
 #pragma unroll
           for (int i = 0; i < 16; ++i)
-            if (c0 + i < cols)
-              store_y(a, static_cast<int64_t>(n0 + c0 + i) * a.y_stride + o,
-                      static_cast<float>(v[i]) * __ldg(a.xs + n0 + c0 + i) * ws);
+            if (c0 + i < cols) store_y(a, static_cast<int64_t>(n0 + c0 + i) * a.y_stride + o, static_cast<float>(v[i]) * xs[i] * ws);
         }
       }
       asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
@@ -409,10 +410,13 @@ __global__ void __launch_bounds__(kGemmThreads) gemm_i8_kernel(const __grid_cons
       const int o = (first % a.m_tiles) * kBM + row, n0 = (first / a.m_tiles) * BN;
       const int cols = min(BN, a.n - n0);
       if (o < a.out) {
-        const float ws = __ldg(a.ws + o);
+        const float ws = a.ws[o];
         // four columns' sums of every CTA at a time: a load from a peer takes as long as one from L2
         for (int c0 = part; c0 < cols; c0 += 4 * a.split) {
           int v[4][8];
+          float xs[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) xs[i] = c0 + i * a.split < cols ? a.xs[n0 + c0 + i * a.split] : 0.0f;
 #pragma unroll
           for (int i = 0; i < 4; ++i)
 #pragma unroll
@@ -425,7 +429,7 @@ __global__ void __launch_bounds__(kGemmThreads) gemm_i8_kernel(const __grid_cons
             int sum = 0;
 #pragma unroll
             for (int r = 0; r < 8; ++r) sum += v[i][r];
-            store_y(a, static_cast<int64_t>(n0 + c) * a.y_stride + o, static_cast<float>(sum) * __ldg(a.xs + n0 + c) * ws);
+            store_y(a, static_cast<int64_t>(n0 + c) * a.y_stride + o, static_cast<float>(sum) * xs[i] * ws);
           }
         }
       }
@@ -658,7 +662,7 @@ __global__ void __launch_bounds__(kPairThreads) gemm_i8_pair_kernel(const __grid
       const int buf = tile % ACC;
       __syncwarp();
 #pragma unroll
-      for (int i = lane; i < BN / 2; i += 32) scales[i] = o0 + i < a.out ? __ldg(a.ws + o0 + i) : 0.0f;
+      for (int i = lane; i < BN / 2; i += 32) scales[i] = o0 + i < a.out ? a.ws[o0 + i] : 0.0f;
       __syncwarp();
       ok = mbar_wait_unless(acc_full(buf), (tile / ACC) & 1, kWaitLimitNs, stop);
       ok = __all_sync(kFull, ok);
@@ -668,7 +672,7 @@ __global__ void __launch_bounds__(kPairThreads) gemm_i8_pair_kernel(const __grid
       }
       asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
       const uint32_t addr = tmem + buf * BN + half * (BN / 2) + (static_cast<uint32_t>(quarter * 32) << 16);
-      const float xs = tok < a.n ? __ldg(a.xs + tok) : 0.0f;
+      const float xs = tok < a.n ? a.xs[tok] : 0.0f;
       const int64_t row = static_cast<int64_t>(tok) * a.y_stride;
       const int rows = a.n - (tok - lane);  // that exist from the warp's first on
       for (int c = 0; c < BN / 2 && o0 + c < a.out; c += 16) {

@@ -327,7 +327,7 @@ __global__ void __launch_bounds__(kWarps * 32, resident_ctas(NT)) kv_attention_k
   const int32_t* table = kv.table + b * kv.table_stride;
   const uint8_t* head = kv.pages + static_cast<int64_t>(2 * h) * kv.block_bytes + copy_src;
   // page number of the lane's piece of tile i (past the end: the last page)
-  auto page_of = [&](int i) { return __ldg(table + min((i * kTile + piece * piece_tokens) >> kv.page_shift, last_page)); };
+  auto page_of = [&](int i) { return table[min((i * kTile + piece * piece_tokens) >> kv.page_shift, last_page)]; };
   auto ask = [&](int i, int pid) {
     const int s = filled % kStages;
     const bool ok = pid >= 0 && pid < kv.n_pages;

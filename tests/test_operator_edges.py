@@ -172,3 +172,60 @@ def test_attention_ends_when_a_wait_runs_out_and_works_again(lens, heads, group,
 
 def test_stall_hook_refuses_bad_devices():
     assert Q.lib().stagq_debug_stall_ops(-1, 0) == EINVAL and Q.lib().stagq_debug_stall_ops(64, 0) == EINVAL
+
+
+# ----------------------------------------- what an earlier kernel of the stream writes
+
+def test_kernels_read_inputs_of_earlier_kernels_with_plain_loads():
+    """The operators are launched before the kernel ahead of them in the stream
+    has ended (programmatic dependent launch), so data that it writes changes
+    within their lifetime: the read-only path, which must not see such data, is
+    not for them."""
+    import os
+    csrc = os.path.join(os.path.dirname(Q.__file__), "csrc")
+    for name in ("gemm_i8.cu", "kv_cache.cu", "kv_attention.cu", "ops_common.cuh"):
+        with open(os.path.join(csrc, name)) as f:
+            text = f.read()
+        assert "ld.global.nc" not in text and "__ldg" not in text, name
+
+
+@gpu
+@pytest.mark.parametrize("n", [3, 40, 300])
+def test_buffers_used_again_by_the_next_call(n):
+    # a layer after another through the same xq, xscale and page table, each step written by the kernel before it
+    inp, out, layers = 1024, 900, 12
+    g = torch.Generator().manual_seed(n)
+    xs = [(torch.randn(n, inp, generator=g) * 2.0 ** (i % 5)).to(F16).cuda() for i in range(layers)]
+    w = torch.randint(-127, 128, (out, inp), generator=g, dtype=torch.int8).cuda()
+    ws = torch.rand(out, generator=g).cuda() * 0.01
+    xq, xscale = torch.empty(n, inp, dtype=torch.int8, device="cuda"), torch.empty(n, device="cuda")
+    want, got = [], [torch.empty(n, out, device="cuda") for _ in xs]
+    for x in xs:
+        q, s, y = torch.empty_like(xq), torch.empty_like(xscale), torch.empty(n, out, device="cuda")
+        Q.stagq_quantize_i8(x, q, s)
+        torch.cuda.synchronize()
+        Q.stagq_gemm_i8(q, s, w, ws, inp, y)
+        torch.cuda.synchronize()
+        want.append(y)
+
+    def chain():
+        for x, y in zip(xs, got):
+            Q.stagq_quantize_i8(x, xq, xscale)
+            Q.stagq_gemm_i8(xq, xscale, w, ws, inp, y)
+
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        chain()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        chain()
+    for _ in range(5):
+        for y in got:
+            y.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        for a, b in zip(got, want):
+            assert torch.equal(a, b)
+    Q.stagq_ops_check(0)
