@@ -461,13 +461,13 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 1) gemv_kernel(const GemvKerne
         const int t = t0 + q * nthreads + tid;
         raw[q][0] = raw[q][1] = make_uint4(0u, 0u, 0u, 0u);
         if (t < ntask) {  // x is [NB][in]: task t of the flat list reads 16 values from 16 t on
-          raw[q][0] = __ldg(x4 + 2 * t);
-          raw[q][1] = __ldg(x4 + 2 * t + 1);
+          raw[q][0] = x4[2 * t];
+          raw[q][1] = x4[2 * t + 1];
         }
         if constexpr (SC) {  // the scale of the task's channels (16 (t mod tpv) on)
           const int ts = t < ntask ? t % tpv : 0;
 #pragma unroll
-          for (int k = 0; k < 4; ++k) sv[q][k] = __ldg(s4 + 4 * ts + k);
+          for (int k = 0; k < 4; ++k) sv[q][k] = s4[4 * ts + k];
         }
       }
       if (t0 == 0 && tid == 0)

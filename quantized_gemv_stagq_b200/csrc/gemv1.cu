@@ -366,12 +366,12 @@ __global__ void __maxnreg__(kRegs1) gemv1_kernel(const Gemv1Args a) {
         const int t = t0 + q * nthreads + tid;
         raw[q][0] = raw[q][1] = make_uint4(0u, 0u, 0u, 0u);
         if (t < ntask) {
-          raw[q][0] = __ldg(x4 + 2 * t);
-          raw[q][1] = __ldg(x4 + 2 * t + 1);
+          raw[q][0] = x4[2 * t];
+          raw[q][1] = x4[2 * t + 1];
         }
         if constexpr (SC) {
 #pragma unroll
-          for (int k = 0; k < 4; ++k) sv[q][k] = t < ntask ? __ldg(s4 + 4 * (t % tpv) + k) : make_float4(0.f, 0.f, 0.f, 0.f);
+          for (int k = 0; k < 4; ++k) sv[q][k] = t < ntask ? s4[4 * (t % tpv) + k] : make_float4(0.f, 0.f, 0.f, 0.f);
         }
       }
 #pragma unroll

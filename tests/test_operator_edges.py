@@ -229,3 +229,15 @@ def test_buffers_used_again_by_the_next_call(n):
         for a, b in zip(got, want):
             assert torch.equal(a, b)
     Q.stagq_ops_check(0)
+
+
+def test_gemv_reads_activations_of_earlier_kernels_with_plain_loads():
+    # x and its inverse scale; a handle's own low values are constant and may take the read-only path
+    import os
+    import re
+    csrc = os.path.join(os.path.dirname(Q.__file__), "csrc")
+    for name in ("gemv.cu", "gemv1.cu", "kernel_common.cuh"):
+        with open(os.path.join(csrc, name)) as f:
+            text = f.read()
+        assert "ld.global.nc" not in text, name
+        assert set(re.findall(r"__ldg\((\S+)", text)) <= {"dlo", "pc.dlo"}, name
