@@ -17,6 +17,7 @@ int bad(const char* what) { return fail(STAGQ_EINVAL, what); }
 
 int launched(cudaError_t e, const char* what) {
   if (e == cudaSuccess) return STAGQ_OK;
+  cudaGetLastError();  // reported here; not left for the caller's next call
   return fail(STAGQ_ECUDA, std::string(what) + ": " + cudaGetErrorString(e));
 }
 

@@ -76,6 +76,7 @@ struct OpsDevice {
   explicit OpsDevice(int dev) {
     ok = cudaGetDevice(&prev) == cudaSuccess && (prev == dev || cudaSetDevice(dev) == cudaSuccess);
     if (prev == dev) prev = -1;
+    if (!ok) cudaGetLastError();  // reported by the call; not left for the caller's next one
   }
   ~OpsDevice() {
     if (prev >= 0) cudaSetDevice(prev);

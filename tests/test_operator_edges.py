@@ -241,3 +241,22 @@ def test_gemv_reads_activations_of_earlier_kernels_with_plain_loads():
             text = f.read()
         assert "ld.global.nc" not in text, name
         assert set(re.findall(r"__ldg\((\S+)", text)) <= {"dlo", "pc.dlo"}, name
+
+
+# ------------------------------------------------------------------- errors
+
+@gpu
+def test_a_call_that_cuda_refuses_leaves_no_error_behind_for_the_next():
+    x, q, s = torch.ones(2, 64, dtype=F16, device="cuda"), torch.empty(2, 128, dtype=torch.int8, device="cuda"), torch.empty(2, device="cuda")
+    if torch.cuda.device_count() > 63:
+        pytest.skip("device 63 exists")
+    L = Q.lib()
+    args = x.data_ptr(), 64, 2, 64, 0, q.data_ptr(), s.data_ptr()
+    for _ in range(2):
+        assert L.stagq_quantize_i8(*args, 63, None) not in (0, EINVAL)  # no such GPU
+        assert L.stagq_ops_check(63) not in (0, EINVAL)
+        assert float((x + 1).sum()) == 256.0  # torch looks for a pending error after its own launch
+        Q.stagq_ops_check(0)
+        assert L.stagq_quantize_i8(*args, 0, None) == 0
+        Q.stagq_ops_check(0)
+        assert (q[:, :64] == 127).all()
