@@ -690,6 +690,8 @@ def stagq_kv_attention_workspace(cache: KVCache, batch: int, max_len: int, q_hea
         n = int(lib().stagq_kv_attention_workspace(cache._c, batch, max_len, q_heads, n_new, int(tracked)))
         if n < 0:
             raise ValueError(f"stagq_kv_attention_workspace: {lib().stagq_last_error().decode()}")
+        if len(cache._workspace) >= 256:  # a program whose max_len follows the lengths
+            cache._workspace.clear()
         cache._workspace[key] = n
     return n
 

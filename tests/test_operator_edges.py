@@ -260,3 +260,12 @@ def test_a_call_that_cuda_refuses_leaves_no_error_behind_for_the_next():
         assert L.stagq_quantize_i8(*args, 0, None) == 0
         Q.stagq_ops_check(0)
         assert (q[:, :64] == 127).all()
+
+
+@gpu
+def test_workspace_sizes_are_not_kept_for_every_length():
+    c = Case([5], 2, 128, 64, 128, F16, width=64)
+    sizes = [Q.stagq_kv_attention_workspace(c.cache, 1, n, 8, tracked=True) for n in range(1, 4097)]
+    held = [v for v in vars(c.cache).values() if isinstance(v, dict)]
+    assert sum(len(d) for d in held) <= 256
+    assert sizes == [Q.stagq_kv_attention_workspace(c.cache, 1, n, 8, tracked=True) for n in range(1, 4097)]
