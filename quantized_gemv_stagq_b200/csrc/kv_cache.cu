@@ -602,13 +602,13 @@ __global__ void __launch_bounds__(256) kv_move_kernel(const __grid_constant__ Kv
 namespace {
 
 // Tokens of a CTA: up to four items per thread, but CTAs for the whole GPU first.
-int row_ctas(KvRowsArgs& a) {
+int row_ctas(KvRowsArgs& a, int num_sms) {
   a.groups = a.kv.dim / a.kv.group;
   a.group_shift = a.kv.group == 128 ? 4 : a.kv.group == 64 ? 3 : 2;
   a.per_token = Divider(static_cast<uint32_t>(a.kv.heads * (a.kv.dim / 8)));
   a.per_sequence = Divider(static_cast<uint32_t>(a.n));
   const int64_t items = a.n_rows * a.per_token.d;
-  int64_t per_cta = items / (148 * 8);
+  int64_t per_cta = items / (num_sms * 8);
   per_cta = per_cta < kRowThreads ? kRowThreads : per_cta > 4 * kRowThreads ? 4 * kRowThreads : per_cta;
   a.cta_tokens = static_cast<int32_t>((per_cta + a.per_token.d - 1) / a.per_token.d);
   return static_cast<int>((a.n_rows + a.cta_tokens - 1) / a.cta_tokens);
@@ -616,13 +616,13 @@ int row_ctas(KvRowsArgs& a) {
 
 }  // namespace
 
-cudaError_t launch_kv_append(KvRowsArgs a, cudaStream_t s) {
-  const dim3 grid(row_ctas(a)), block(kRowThreads);
+cudaError_t launch_kv_append(KvRowsArgs a, int num_sms, cudaStream_t s) {
+  const dim3 grid(row_ctas(a, num_sms)), block(kRowThreads);
   return a.kv.bf16 ? launch_op(kv_append_kernel<true>, grid, block, 0, s, a) : launch_op(kv_append_kernel<false>, grid, block, 0, s, a);
 }
 
-cudaError_t launch_kv_read(KvRowsArgs a, cudaStream_t s) {
-  const dim3 grid(row_ctas(a)), block(kRowThreads);
+cudaError_t launch_kv_read(KvRowsArgs a, int num_sms, cudaStream_t s) {
+  const dim3 grid(row_ctas(a, num_sms)), block(kRowThreads);
   if (a.f32)
     return a.kv.bf16 ? launch_op(kv_read_kernel<true, true>, grid, block, 0, s, a) : launch_op(kv_read_kernel<false, true>, grid, block, 0, s, a);
   return a.kv.bf16 ? launch_op(kv_read_kernel<true, false>, grid, block, 0, s, a) : launch_op(kv_read_kernel<false, false>, grid, block, 0, s, a);

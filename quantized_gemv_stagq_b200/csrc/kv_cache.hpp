@@ -93,8 +93,8 @@ struct KvAttnPlan {
 KvAttnPlan plan_kv_attention(int batch, int heads, int q_heads, int n_new, int dim, int max_len, bool mass,
                              int num_sms);
 
-cudaError_t launch_kv_append(KvRowsArgs a, cudaStream_t s);
-cudaError_t launch_kv_read(KvRowsArgs a, cudaStream_t s);
+cudaError_t launch_kv_append(KvRowsArgs a, int num_sms, cudaStream_t s);
+cudaError_t launch_kv_read(KvRowsArgs a, int num_sms, cudaStream_t s);
 cudaError_t launch_kv_attention(const KvAttnArgs& a, const KvAttnPlan& p, cudaStream_t s);
 cudaError_t launch_kv_evict(KvEvictArgs a, int num_sms, cudaStream_t s);
 

@@ -29,7 +29,7 @@ constexpr int kMaxDevices = 64;
 
 // Multiprocessors of the current device `device`; 0 if the query fails.
 int sm_count(int device) {
-  static int known[kMaxDevices] = {};  // a racing first call stores the same number
+  static std::atomic<int> known[kMaxDevices];  // a racing first call stores the same number
   if (!known[device]) {
     int n = 0;
     if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, device) != cudaSuccess) {
@@ -194,7 +194,9 @@ extern "C" int stagq_kv_append(const stagq_kv_cache* c, const stagq_kv_table* t,
   a.n = n;
   a.n_rows = static_cast<int64_t>(t->batch) * n;
   a.vec = wide(k, k_stride, 2) && wide(v, v_stride, 2);
-  return launched(launch_kv_append(a, static_cast<cudaStream_t>(cuda_stream)), "append launch");
+  const int sms = sm_count(c->device);
+  if (!sms) return fail(STAGQ_ENODEV, "no usable device");
+  return launched(launch_kv_append(a, sms, static_cast<cudaStream_t>(cuda_stream)), "append launch");
 }
 
 extern "C" int stagq_kv_read(const stagq_kv_cache* c, const stagq_kv_table* t, const int32_t* starts,
@@ -216,7 +218,9 @@ extern "C" int stagq_kv_read(const stagq_kv_cache* c, const stagq_kv_table* t, c
   a.n_rows = static_cast<int64_t>(t->batch) * n;
   a.f32 = (flags & STAGQ_Y_F32) ? 1 : 0;
   a.vec = wide(k, k_stride, a.f32 ? 4 : 2) && wide(v, v_stride, a.f32 ? 4 : 2);
-  return launched(launch_kv_read(a, static_cast<cudaStream_t>(cuda_stream)), "read launch");
+  const int sms = sm_count(c->device);
+  if (!sms) return fail(STAGQ_ENODEV, "no usable device");
+  return launched(launch_kv_read(a, sms, static_cast<cudaStream_t>(cuda_stream)), "read launch");
 }
 
 namespace {
