@@ -557,6 +557,20 @@ int stagq_debug_stall(stagq_handle h, uint32_t stall_ns);
 int stagq_debug_stall_ops(int device, uint32_t stall_ns);
 
 /*
+ * Test hooks: how stagq_gemm_i8 and stagq_kv_attention split such a call over
+ * num_sms multiprocessors (computed on the host; no device is needed).
+ *   plan of the product    tokens per tile (of a pair: channels), CTAs that share
+ *                          a tile's K, 1 for pairs of CTAs, CTAs of the launch
+ *   plan of the attention  query rows of a unit, units of a KV head, CTAs of the
+ *                          launch, CTAs per unit (0: all rounds of 128 tokens are
+ *                          dealt evenly to the CTAs, and a second kernel joins)
+ * Errors: STAGQ_EINVAL.
+ */
+int stagq_debug_gemm_i8_plan(int32_t n, int32_t out, int32_t in, int32_t num_sms, int32_t plan[4]);
+int stagq_debug_kv_attention_plan(const stagq_kv_cache* cache, int32_t batch, int32_t max_len, int32_t q_heads,
+                                  int32_t n_new, int tracked, int32_t num_sms, int32_t plan[4]);
+
+/*
  * Where the handle's side record lives on the device: the loader re-lays the
  * CSR record (Eq. 4) per CTA for each kernel's grid.
  *   General kernel (grid CTAs, stride bytes each): CTA b owns rows

@@ -114,6 +114,8 @@ _SIGNATURES = {
                                       _c_p, _i64, _i64, _i32, _c_p]),
     "stagq_ops_check": (ctypes.c_int, [ctypes.c_int]),
     "stagq_debug_stall_ops": (ctypes.c_int, [ctypes.c_int, _u32]),
+    "stagq_debug_gemm_i8_plan": (ctypes.c_int, [_i32, _i32, _i32, _i32, ctypes.POINTER(_i32)]),
+    "stagq_debug_kv_attention_plan": (ctypes.c_int, [_CACHE_P, _i32, _i32, _i32, _i32, ctypes.c_int, _i32, ctypes.POINTER(_i32)]),
     "stagq_free": (None, [_c_p]),
     "stagq_strerror": (ctypes.c_char_p, [ctypes.c_int]),
     "stagq_last_error": (ctypes.c_char_p, []),
@@ -780,3 +782,20 @@ def stagq_ops_check(device: int = 0) -> None:
 def stagq_debug_stall_ops(device: int, stall_ns: int) -> None:
     """Test hook: the operators launched on the device give up a wait of stall_ns; 0 turns it off."""
     _check(lib().stagq_debug_stall_ops(device, stall_ns), "stagq_debug_stall_ops")
+
+
+def stagq_debug_gemm_i8_plan(n: int, out: int, inp: int, num_sms: int):
+    """Test hook: (tile width, CTAs that share a tile's K, pairs, CTAs) of such a stagq_gemm_i8."""
+    plan = (_i32 * 4)()
+    _check(lib().stagq_debug_gemm_i8_plan(n, out, inp, num_sms, plan), "stagq_debug_gemm_i8_plan")
+    return tuple(plan)
+
+
+def stagq_debug_kv_attention_plan(heads: int, dim: int, page: int, group: int, batch: int, max_len: int, q_heads: int,
+                                  n_new: int, tracked: bool, num_sms: int):
+    """Test hook: (rows of a unit, units of a KV head, CTAs, CTAs per unit or 0) of such a stagq_kv_attention."""
+    plan = (_i32 * 4)()
+    cache = _KvCache(None, 1, heads, dim, page, group, 0, 0)
+    _check(lib().stagq_debug_kv_attention_plan(cache, batch, max_len, q_heads, n_new, int(tracked), num_sms, plan),
+           "stagq_debug_kv_attention_plan")
+    return tuple(plan)

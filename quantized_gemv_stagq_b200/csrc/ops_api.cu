@@ -384,3 +384,26 @@ extern "C" int stagq_debug_stall_ops(int device, uint32_t stall_ns) {
   g_stall_ns[device] = stall_ns;
   return STAGQ_OK;
 }
+
+extern "C" int stagq_debug_gemm_i8_plan(int32_t n, int32_t out, int32_t in, int32_t num_sms, int32_t* plan) {
+  const int64_t ld = stagq_i8_row_bytes(in);
+  if (ld < 0 || n < 1 || out < 1 || num_sms < 2 || !plan) return bad("bad sizes or null plan");
+  const GemmI8Plan p = plan_gemm_i8(n, out, static_cast<int>(ld / STAGQ_I8_ROW_MULTIPLE), num_sms);
+  plan[0] = p.bn;
+  plan[1] = p.split;
+  plan[2] = p.pair;
+  plan[3] = p.grid;
+  return STAGQ_OK;
+}
+
+extern "C" int stagq_debug_kv_attention_plan(const stagq_kv_cache* c, int32_t batch, int32_t max_len, int32_t q_heads,
+                                             int32_t n_new, int tracked, int32_t num_sms, int32_t* plan) {
+  if (const char* e = attention_error(c, batch, max_len, q_heads, n_new)) return bad(e);
+  if (num_sms < 1 || !plan) return bad("no multiprocessors or null plan");
+  const KvAttnPlan p = plan_kv_attention(batch, c->heads, q_heads, n_new, c->dim, max_len, tracked != 0, num_sms);
+  plan[0] = 4 * p.nt;
+  plan[1] = p.row_blocks;
+  plan[2] = p.ctas;
+  plan[3] = p.cluster;
+  return STAGQ_OK;
+}
