@@ -4,19 +4,20 @@
 //   q_ik = rint(127 x_ik / a_i), a_i = max_k |x_ik|, scale_i = a_i / 127
 //   y_ij = scale_i wscale_j sum_k q_ik w_jk        (the sum exact in int32)
 //
-// The product runs on the tcgen05 tensor cores (kind::i8): the weights' 128
-// output channels are the accumulator's 128 lanes, BN tokens its columns, so
-// few tokens cost few columns and the weights are always the wide operand.
-// TMA brings 128-byte K blocks of both operands into a ring of 128B-swizzled
-// stages; one thread issues the MMAs; four warps read the int32 accumulators
-// from TMEM, scale and store (32 consecutive channels of one token per store).
-//
-// Many tokens (BN = 128 or 256): persistent CTAs, one per SM, two accumulators,
-// so that a tile's epilogue runs under the next tile's MMAs. Bound by the
-// tensor cores. Few tokens (BN = 16, 32, 64): bound by the weights' bytes; a
-// cluster of up to 8 CTAs shares one tile's K so that all SMs stream, and adds
-// its partial sums through distributed shared memory. The partial sums are
-// integers, so the split changes no bit of the result.
+// The product runs on the tcgen05 tensor cores (kind::i8). TMA brings 128-byte
+// K blocks of both operands into a ring of 128B-swizzled stages; one thread
+// issues the MMAs; the other warps read the int32 accumulators from TMEM, scale
+// and store. Two kernels, chosen from the sizes by plan_gemm_i8:
+//  - gemm_i8_kernel, few tokens: 128 output channels are the accumulator's
+//    lanes and 16, 32 or 64 tokens its columns, so few tokens cost few columns.
+//    A CTA has one tile, and two CTAs share an SM. Bound by the weights' bytes;
+//    a cluster of up to 8 CTAs shares one tile's K so that all SMs stream, and
+//    adds its partial sums through distributed shared memory. They are
+//    integers, so the split changes no bit of the result.
+//  - gemm_i8_pair_kernel, many tokens: persistent pairs of CTAs (cta_group::2)
+//    on tiles of 256 tokens and 128 or 256 channels, tokens as lanes, with two
+//    accumulators, so that a tile's epilogue runs under the next tile's MMAs.
+//    Bound by the tensor cores.
 #include <cuda.h>
 
 #include <algorithm>
@@ -150,12 +151,9 @@ constexpr int kGemmThreads = 192;      // TMA warp, MMA warp, four epilogue warp
 constexpr uint64_t kWaitLimitNs = 2000000000ull;
 
 __host__ __device__ constexpr int stage_bytes(int bn) { return (kBM + bn) * kBK; }
-// Stages of the ring: two CTAs share an SM up to 64 tokens, one has it to itself above.
-__host__ __device__ constexpr int stage_count(int bn) {
-  return bn == 16 ? 6 : bn == 32 ? 5 : bn == 64 ? 4 : bn == 128 ? 6 : 4;
-}
-__host__ __device__ constexpr int acc_count(int bn) { return bn >= 128 ? 2 : 1; }
-__host__ __device__ constexpr int tmem_cols(int bn) { return bn * acc_count(bn) < 32 ? 32 : bn * acc_count(bn); }
+// Stages of the ring: two CTAs share an SM.
+__host__ __device__ constexpr int stage_count(int bn) { return bn == 16 ? 6 : bn == 32 ? 5 : 4; }
+__host__ __device__ constexpr int tmem_cols(int bn) { return bn < 32 ? 32 : bn; }
 constexpr int kBarrierBytes = 256;
 __host__ __device__ constexpr size_t gemm_smem(int bn) {
   return 1024 + static_cast<size_t>(stage_count(bn)) * stage_bytes(bn) + kBarrierBytes;
@@ -218,9 +216,6 @@ __device__ __forceinline__ void mma_commit_pair_here(uint32_t bar) {
 __device__ __forceinline__ void mbar_arrive_cluster(uint32_t bar) {
   asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
-__device__ __forceinline__ void mbar_arrive(uint32_t bar) {
-  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
-}
 __device__ __forceinline__ void tmem_load16(uint32_t addr, int (&v)[16]) {
   asm volatile(
       "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
@@ -251,7 +246,7 @@ template <int BN>
 __global__ void __launch_bounds__(kGemmThreads) gemm_i8_kernel(const __grid_constant__ GemmI8Args a,
                                                               const __grid_constant__ CUtensorMap wmap,
                                                               const __grid_constant__ CUtensorMap xmap) {
-  constexpr int STAGES = stage_count(BN), ACC = acc_count(BN);
+  constexpr int STAGES = stage_count(BN);
   extern __shared__ uint8_t smem_raw[];
   __shared__ uint32_t s_tmem;
   __shared__ uint32_t s_stop;
@@ -261,9 +256,7 @@ __global__ void __launch_bounds__(kGemmThreads) gemm_i8_kernel(const __grid_cons
   const uint32_t bars = ring + STAGES * stage_bytes(BN);
   auto full = [&](int s) { return bars + 8 * s; };
   auto empty = [&](int s) { return bars + 8 * (STAGES + s); };
-  auto acc_full = [&](int s) { return bars + 8 * (2 * STAGES + s); };
-  auto acc_empty = [&](int s) { return bars + 8 * (2 * STAGES + ACC + s); };
-  const uint32_t drained = bars + 8 * (2 * STAGES + 2 * ACC);
+  const uint32_t acc_full = bars + 8 * (2 * STAGES), drained = bars + 8 * (2 * STAGES + 1);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
   if (threadIdx.x == 0) {
@@ -273,10 +266,7 @@ __global__ void __launch_bounds__(kGemmThreads) gemm_i8_kernel(const __grid_cons
       mbar_init(full(s), 1);
       mbar_init(empty(s), 1);
     }
-    for (int s = 0; s < ACC; ++s) {
-      mbar_init(acc_full(s), 1);
-      mbar_init(acc_empty(s), 128);
-    }
+    mbar_init(acc_full, 1);
     mbar_init(drained, 1);
     s_stop = 0;
     fence_barrier_init();
@@ -299,7 +289,7 @@ __global__ void __launch_bounds__(kGemmThreads) gemm_i8_kernel(const __grid_cons
   const int part = blockIdx.x % a.split;
   const int k0 = static_cast<int>(static_cast<int64_t>(a.kblocks) * part / a.split);
   const int k1 = static_cast<int>(static_cast<int64_t>(a.kblocks) * (part + 1) / a.split);
-  const int n_work = a.m_tiles * a.n_tiles, first = blockIdx.x / a.split, step = gridDim.x / a.split;
+  const int tile = blockIdx.x / a.split, m0 = (tile % a.m_tiles) * kBM, n0 = (tile / a.m_tiles) * BN;
   auto give_up = [&]() {
     s_stop = 1;
     __threadfence_block();
@@ -314,72 +304,49 @@ __global__ void __launch_bounds__(kGemmThreads) gemm_i8_kernel(const __grid_cons
 
   if (warp == 0) {
     if (lane == 0) {
-      uint32_t it = 0;
       bool ok = !stalled(0);
-      for (int w = first; w < n_work && ok; w += step) {
-        const int m0 = (w % a.m_tiles) * kBM, n0 = (w / a.m_tiles) * BN;
-        for (int k = k0; k < k1; ++k, ++it) {
-          const int s = it % STAGES;
-          if (!mbar_wait_unless(empty(s), ((it / STAGES) & 1) ^ 1, kWaitLimitNs, stop)) {
-            ok = false;
-            break;
-          }
-          const uint32_t dst = ring + s * stage_bytes(BN);
-          mbar_arrive_expect_tx(full(s), stage_bytes(BN));
-          tma_load_2d(dst, &wmap, k * kBK, m0, full(s));
-          tma_load_2d(dst + kBM * kBK, &xmap, k * kBK, n0, full(s));
-        }
+      for (int k = k0; k < k1 && ok; ++k) {
+        const int s = issued % STAGES;
+        ok = mbar_wait_unless(empty(s), ((issued / STAGES) & 1) ^ 1, kWaitLimitNs, stop);
+        if (!ok) break;
+        const uint32_t dst = ring + s * stage_bytes(BN);
+        mbar_arrive_expect_tx(full(s), stage_bytes(BN));
+        tma_load_2d(dst, &wmap, k * kBK, m0, full(s));
+        tma_load_2d(dst + kBM * kBK, &xmap, k * kBK, n0, full(s));
+        ++issued;
       }
       if (!ok) give_up();
-      issued = it;
     }
   } else if (warp == 1) {
     if (lane == 0) {
       constexpr uint32_t idesc = instr_desc(BN, kBM);
-      uint32_t it = 0, tile = 0;
       bool ok = !stalled(1);
-      for (int w = first; w < n_work && ok; w += step, ++tile) {
-        const int buf = tile % ACC;
-        if (!mbar_wait_unless(acc_empty(buf), ((tile / ACC) & 1) ^ 1, kWaitLimitNs, stop)) {
-          ok = false;
-          break;
-        }
+      for (int k = k0; k < k1 && ok; ++k) {
+        const int it = k - k0, s = it % STAGES;
+        ok = mbar_wait_unless(full(s), (it / STAGES) & 1, kWaitLimitNs, stop);
+        if (!ok) break;
         asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-        for (int k = k0; k < k1; ++k, ++it) {
-          const int s = it % STAGES;
-          if (!mbar_wait_unless(full(s), (it / STAGES) & 1, kWaitLimitNs, stop)) {
-            ok = false;
-            break;
-          }
-          asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-          const uint64_t ad = smem_desc(ring + s * stage_bytes(BN)), bd = smem_desc(ring + s * stage_bytes(BN) + kBM * kBK);
+        const uint64_t ad = smem_desc(ring + s * stage_bytes(BN)), bd = smem_desc(ring + s * stage_bytes(BN) + kBM * kBK);
 #pragma unroll
-          for (int i = 0; i < kBK / 32; ++i)  // 32 bytes of K per MMA: 2 units of the descriptor's address
-            mma_i8(tmem + buf * BN, ad + 2 * i, bd + 2 * i, idesc, k > k0 || i > 0);
-          mma_commit(empty(s));
-        }
-        if (ok) mma_commit(acc_full(buf));
+        for (int i = 0; i < kBK / 32; ++i)  // 32 bytes of K per MMA: 2 units of the descriptor's address
+          mma_i8(tmem, ad + 2 * i, bd + 2 * i, idesc, it > 0 || i > 0);
+        mma_commit(empty(s));
       }
-      if (!ok) give_up();
+      if (ok)
+        mma_commit(acc_full);
+      else
+        give_up();
     }
   } else {
     const int quarter = warp & 3;  // the TMEM lanes that this warp may read
-    const int row = quarter * 32 + lane;
-    uint32_t tile = 0;
-    bool ok = !__any_sync(kFull, stalled(2));
-    if (!ok && lane == 0) give_up();
-    for (int w = first; w < n_work && ok; w += step, ++tile) {
-      const int o = (w % a.m_tiles) * kBM + row, n0 = (w / a.m_tiles) * BN;
-      const int cols = min(BN, a.n - n0);
-      const int buf = tile % ACC;
-      ok = mbar_wait_unless(acc_full(buf), (tile / ACC) & 1, kWaitLimitNs, stop);
-      ok = __all_sync(kFull, ok);
-      if (!ok) {
-        if (lane == 0) give_up();
-        break;
-      }
+    const int row = quarter * 32 + lane, o = m0 + row, cols = min(BN, a.n - n0);
+    bool ok = !stalled(2) && mbar_wait_unless(acc_full, 0, kWaitLimitNs, stop);
+    ok = __all_sync(kFull, ok);
+    if (!ok) {
+      if (lane == 0) give_up();
+    } else {
       asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-      const uint32_t addr = tmem + buf * BN + (static_cast<uint32_t>(quarter * 32) << 16);
+      const uint32_t addr = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
       const float ws = o < a.out ? a.ws[o] : 0.0f;
       for (int c0 = 0; c0 < cols; c0 += 16) {
         int v[16];
@@ -398,17 +365,13 @@ __global__ void __launch_bounds__(kGemmThreads) gemm_i8_kernel(const __grid_cons
             if (c0 + i < cols) store_y(a, static_cast<int64_t>(n0 + c0 + i) * a.y_stride + o, static_cast<float>(v[i]) * xs[i] * ws);
         }
       }
-      asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
-      mbar_arrive(acc_empty(buf));
     }
   }
-  if (a.split > 1) {  // one tile per cluster
+  if (a.split > 1) {
     __syncwarp();
     cluster_sync_all();
     if (warp >= 2 && !*stop) {
-      const int row = (warp & 3) * 32 + lane;
-      const int o = (first % a.m_tiles) * kBM + row, n0 = (first / a.m_tiles) * BN;
-      const int cols = min(BN, a.n - n0);
+      const int row = (warp & 3) * 32 + lane, o = m0 + row, cols = min(BN, a.n - n0);
       if (o < a.out) {
         const float ws = a.ws[o];
         // four columns' sums of every CTA at a time: a load from a peer takes as long as one from L2
@@ -782,7 +745,7 @@ GemmI8Plan plan_gemm_i8(int n, int out, int kblocks, int num_sms) {
   p.split = 1;
   const int64_t tiles = m_tiles * ((n + p.bn - 1) / p.bn);
   while (p.split < 8 && tiles * p.split * 2 <= 2 * num_sms && kblocks >= 4 * p.split * 2) p.split *= 2;
-  p.grid = static_cast<int>(std::min<int64_t>(tiles * p.split, 1 << 30));
+  p.grid = static_cast<int>(tiles * p.split);
   if (n <= 64) return p;
 
   const int64_t pairs = num_sms / 2, m_pairs = (n + 2 * kBM - 1) / (2 * kBM);
