@@ -464,7 +464,10 @@ def run_extra(args):
         mats = {name: Q.stagq_load_stack([enc[n] for n in members], 0) for name, members in LAYER_LAUNCHES}
         row = 2 * heads * (dim // 2 + 4 * (dim // group))  # a cached token's bytes, K and V
 
-        def graph_us(body, reps):
+        reps, timings = 20, 5
+
+        def graph_us(body, kernels):
+            nonlocal launches
             with torch.cuda.stream(stream):
                 body()
             torch.cuda.synchronize()
@@ -472,7 +475,8 @@ def run_extra(args):
             with torch.cuda.graph(g, stream=stream):
                 for _ in range(reps):
                     body()
-            return _median_event_us(torch, stream, g.replay, 5) / reps
+            launches += kernels * (1 + reps * timings)
+            return _median_event_us(torch, stream, g.replay, timings) / reps
 
         for batch in (1, 4):
             x = {n: torch.from_numpy(synth.activations(batch, m.inp, seed=m.inp)).cuda() for n, m in mats.items()}
@@ -502,9 +506,10 @@ def run_extra(args):
                         Q.stagq_gemv_n(mats[n], bits, x[n], batch, y[n], stream=stream)
 
                 nb = batch * ctx * row
-                for what, us, n in (("attention", graph_us(attention, 20), nb),
-                                    ("step", graph_us(step, 20), nb + sum(Q.stagq_bytes(m, bits, batch) for m in mats.values()))):
-                    launches += 21 * 6 * 6
+                kernels = _attention_launches(ws.numel()) + 1  # and the append
+                for what, us, n in (("attention", graph_us(attention, kernels), nb),
+                                    ("step", graph_us(step, kernels + len(mats)),
+                                     nb + sum(Q.stagq_bytes(m, bits, batch) for m in mats.values()))):
                     results[f"{what} batch{batch} ctx{ctx}"] = {"us": round(us, 2), "bytes": n, "gbs": round(n / us / 1e3, 1),
                                                                 "frac": round(n / us / 1e3 / peak, 4)}
         n = 512
@@ -521,8 +526,7 @@ def run_extra(args):
                 Q.stagq_quantize_i8(xi, xq, xscale, stream=stream)
                 Q.stagq_gemm_i8(xq, xscale, wq, wscale, m.inp, yi, stream=stream)
 
-            us = graph_us(linear, 20)
-            launches += 2 * 21 * 6
+            us = graph_us(linear, 2)
             nb = 2 * n * m.inp + m.out * m.inp + 2 * n * m.out
             results[f"i8 {name} {m.out}x{m.inp} tokens{n}"] = {
                 "us": round(us, 2), "bytes": nb, "tflops": round(2e-6 * n * m.inp * m.out / us, 1),
@@ -606,6 +610,12 @@ def run_extra(args):
 # stacked (they share x), down -- each on its own input.
 LAYER_LAUNCHES = [("qkv", ("q_proj", "k_proj", "v_proj")), ("o", ("o_proj",)),
                   ("gate_up", ("gate_proj", "up_proj")), ("down", ("down_proj",))]
+
+
+def _attention_launches(workspace_bytes):
+    """Kernels of one stagq_kv_attention: a call that needs a workspace has its
+    partial sums joined by a second one."""
+    return 2 if workspace_bytes else 1
 
 
 def _median_event_us(torch, stream, fn, repeats):

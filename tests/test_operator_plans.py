@@ -257,3 +257,37 @@ def test_gemm_i8_pairs_use_their_rings_and_accumulators_again(n, inp, out, width
             assert torch.equal(whole[:, first:first + out], want.to(dtype)), (dtype, first)
             assert (whole[:, :first] == 7).all() and (whole[:, first + out:] == 7).all()
     Q.stagq_ops_check(0)
+
+
+# -------------------------------------------------------------------- launches
+
+@gpu
+@pytest.mark.parametrize("lens,tracked", [([777], False), ([4000, 9], False), ([70000], False), ([777], True)])
+def test_launches_that_the_benchmark_counts(lens, tracked):
+    runtime = pytest.importorskip("cuda.bindings.runtime")
+    import bench
+    c = Filled(lens, 2, 128, 64, 128, F16)
+    q = rnd((len(lens), 8 * 128), 5, F16).cuda()
+    need = Q.stagq_kv_attention_workspace(c.cache, len(lens), c.width * 64, 8, 1, tracked)
+    ws, out = torch.empty(max(need, 1), dtype=torch.uint8, device="cuda"), torch.empty_like(q)
+    mass = torch.zeros(len(lens), 2, c.width * 64, device="cuda") if tracked else None
+    k = torch.zeros(len(lens), 2 * 128, dtype=F16, device="cuda")
+    x, xq, xs = torch.zeros(5, 256, dtype=F16, device="cuda"), torch.empty(5, 256, dtype=torch.int8, device="cuda"), torch.empty(5, device="cuda")
+    y = torch.empty(5, 5, device="cuda")
+
+    def attention():
+        Q.stagq_kv_attention(c.cache, q, c.table, c.lens, out, mass=mass, workspace=ws)
+
+    def linear():
+        Q.stagq_quantize_i8(x, xq, xs)
+        Q.stagq_gemm_i8(xq, xs, xq, xs, 256, y)
+
+    starts = c.lens - 1
+    for body, kernels in ((attention, bench._attention_launches(need)), (linear, 2),
+                          (lambda: Q.stagq_kv_append(c.cache, k, k, c.table, starts, 1), 1)):
+        graph = torch.cuda.CUDAGraph(keep_graph=True)
+        with torch.cuda.graph(graph):
+            body()
+        status, _, nodes = runtime.cudaGraphGetNodes(graph.raw_cuda_graph(), 0)
+        assert status == runtime.cudaError_t.cudaSuccess
+        assert nodes == kernels
