@@ -41,7 +41,7 @@ extern "C" {
 #define STAGQ_ECUDA 4    /* a CUDA runtime call failed (detail in stagq_last_error) */
 #define STAGQ_EIO 5      /* file could not be read or written */
 #define STAGQ_ENODEV 6   /* no usable sm_100 device */
-#define STAGQ_ETIMEOUT 7 /* a GEMV kernel gave up waiting for its own copies (reported by stagq_check) */
+#define STAGQ_ETIMEOUT 7 /* a kernel gave up waiting for its own copies (reported by stagq_check, stagq_ops_check) */
 
 /* Limits of this implementation. */
 #define STAGQ_MAX_PLANES 4      /* stream depth N = 2 + n_planes <= 6 (the paper evaluates N = 6) */
@@ -384,7 +384,8 @@ int64_t stagq_i8_row_bytes(int32_t in);
 
 /*
  * Rows rounded to 8 bits with a scale each (activations: a scale per token;
- * weights [out, in]: a scale per output channel):
+ * weights [out, in]: a scale per output channel, from 16-bit weights: there is
+ * no way from a StagQ stream or handle to such rows):
  *   a_i = max_k |x_ik|,  scale_i = a_i / 127,  q_ik = rint(127 x_ik / a_i)
  * with ties to even on the binary64 quotient; a_i = 0 gives q = 0. A row that
  * holds an infinity or a NaN gets scale NaN and q = 0, so that every product
@@ -488,6 +489,13 @@ int stagq_kv_read(const stagq_kv_cache* cache, const stagq_kv_table* table, cons
  *             stagq_kv_attention_workspace() bytes (may be null if that is 0).
  *             Calls that run at the same time need workspaces of their own.
  * A position whose page is not in the pool counts as unseen and is reported.
+ * A prompt: append it whole, then attend STAGQ_KV_MAX_NEW tokens a call, with
+ * lens raised by as many each time; the masses add up. (Each call reads the
+ * cache once for every 8 query rows of a KV head: this serves prompts of some
+ * hundred tokens, and is no replacement for attention over 16-bit K and V.)
+ * Precision: scores, weights and sums are fp32, from the terms s q u and lo q;
+ * p s is summed in parts that drop 2^-30, per token, of the largest scale s of
+ * the sequence's V in that group. Sums stay finite while |V| is below 2^88.
  * Errors: STAGQ_EINVAL, STAGQ_ECUDA.
  */
 int stagq_kv_attention(const stagq_kv_cache* cache, const stagq_kv_table* table, const int32_t* lens, int32_t max_len,

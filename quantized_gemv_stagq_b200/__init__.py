@@ -580,7 +580,7 @@ def stagq_i8_row_bytes(inp: int) -> int:
 def stagq_quantize_i8(x, q, scale, stream=None) -> None:
     """Rows of x [n, inp] (fp16 or bf16) rounded to 8 bits: q int8 [n,
     stagq_i8_row_bytes(inp)], scale fp32 [n]. Serves tokens and, once, the
-    rows of a weight matrix (its output channels)."""
+    rows of a 16-bit weight matrix (its output channels)."""
     dev = _cuda_index(x, "x")
     if x.dim() != 2:
         raise ValueError(f"x must be [n, inp], got {list(x.shape)}")
@@ -704,8 +704,10 @@ def stagq_kv_attention(cache: KVCache, q, table, lens, out, n_new: int = 1, scal
     q, out: [batch * n_new, q_heads * dim]; lens int32 [batch], cached tokens
     with the new ones; scale: 1 / sqrt(dim) unless given; mass fp32 [batch,
     heads, tokens]: adds every token's weights to it. max_len (a bound on
-    lens) defaults to what the table, and the mass, hold. workspace: a uint8
-    tensor of stagq_kv_attention_workspace bytes, else one is allocated."""
+    lens) defaults to what the table, and the mass, hold, and the workspace
+    grows with it. workspace: a uint8 tensor of stagq_kv_attention_workspace
+    bytes, else one is allocated. A prompt: appended whole, attended
+    STAGQ_KV_MAX_NEW tokens a call with lens raised by as many."""
     t = cache._table(table)
     dev = cache.device
     rows = t.batch * n_new

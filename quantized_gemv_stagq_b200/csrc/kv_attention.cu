@@ -7,9 +7,11 @@
 // sum_t (p_t s_t) u_t + sum_t p_t lo_t: the matrix products only ever see the
 // codes u and never a rebuilt K or V.
 //
-// Bound by the cache's bytes as long as the unpacking keeps up: at 6.5 TB/s an
-// SM takes in about 49 codes per clock. What keeps the instruction count near
-// one per two codes:
+// The cache's bytes would bound it if the unpacking kept up: at 6.5 TB/s an SM
+// takes in about 49 codes per clock. Measured, long sequences stream 3.4 TB/s:
+// issue slots 59 % and the ALU pipe 55 % busy, no unit full, 12 warps per SM
+// that each wait on their own chain of steps. What keeps the instruction count
+// near one per two codes:
 //  - V: two codes are masked out of a word in place and OR'ed under the exponent
 //    of 1024 in one operation; a packed subtraction leaves u - 8 (16 times that
 //    for the upper 4 bits of a byte) as exact fp16, and lo + 8 s replaces lo.
@@ -18,7 +20,10 @@
 //  - K: the same bits without the OR are fp16 subnormals, 16 u 2^-24, exact
 //    too, and mma takes them at full rate; nothing needs to be subtracted. It
 //    aligns products by their nominal exponents, which drops what lies below
-//    2^-18 of the row's largest q: of a score, about 1e-6.
+//    2^-18 of the row's largest q. For q of even size that is less than the
+//    rounding of s q u + lo q adds (weights off by 7e-7); where one channel is
+//    2^10 times the others and more, weights were off by 2.4e-5, against 4e-6
+//    for the same sums without the drop.
 //  - The order of a contraction is free, so the packed order of a row is the
 //    order of the mma fragments (kv_cache.cu): a lane's K words feed its
 //    A fragments without a shuffle, and two tokens' V words give the pairs of
@@ -26,9 +31,13 @@
 //  - Tokens are the 16 rows of the first product and the contraction of the
 //    second, query rows the 8 columns: S^T = K q^T and out^T = V^T p^T.
 //  - Of the 8 columns 4 are query rows and 4 repeat them: in the second
-//    product the repeats carry what rounding p s to fp16 lost. The result
-//    then has fp32's error although mma takes fp16, at no extra mma for up to
-//    4 query rows per KV head (32 / 8 and 40 / 10 heads).
+//    product the repeats carry what rounding p s to fp16 lost, at no extra mma
+//    for up to 4 query rows per KV head (32 / 8 and 40 / 10 heads). Together
+//    the parts hold 22 bits of p s above 2^-9 of the largest scale s that the
+//    warp has met in the group, and below that all but 2^-30 of that scale per
+//    token. So the result has fp32's error as long as V's scales lie within
+//    some 2^12 of one another; a token with a larger one leaves the others
+//    fewer bits, also where its own weight is small.
 // The tcgen05 tensor cores would need the codes expanded to 8 or 16 bits in
 // shared memory first, 2 to 4 times the cache's bytes of shared-memory writes
 // and reads, for products that mma.sync does within the bytes' time.

@@ -232,7 +232,7 @@ const char* attention_error(const stagq_kv_cache* c, int32_t batch, int32_t max_
   if (q_heads < 1 || q_heads % c->heads) return "q_heads must be a multiple of the cache's heads";
   if (q_heads / c->heads > STAGQ_KV_MAX_SHARE) return "more than STAGQ_KV_MAX_SHARE query heads per KV head";
   if (n_new < 1 || n_new > STAGQ_KV_MAX_NEW) return "n_new outside 1..STAGQ_KV_MAX_NEW";
-  // the join's grid: rows in blocks of up to 8, and 512 tokens of a head per CTA
+  // the join's grid: rows in blocks of up to 8, and 2048 tokens of a head per CTA (counted here as 512)
   const int64_t heads = static_cast<int64_t>(batch) * c->heads;
   if (heads * (q_heads / c->heads * n_new + 8 + (static_cast<int64_t>(max_len) + 511) / 512) > INT_MAX) return "too many rows for one call";
   // rounds of 128 tokens, numbered through all units

@@ -269,3 +269,28 @@ def test_workspace_sizes_are_not_kept_for_every_length():
     held = [v for v in vars(c.cache).values() if isinstance(v, dict)]
     assert sum(len(d) for d in held) <= 256
     assert sizes == [Q.stagq_kv_attention_workspace(c.cache, 1, n, 8, tracked=True) for n in range(1, 4097)]
+
+
+# ------------------------------------------------------------------ a prompt
+
+@gpu
+def test_a_prompt_is_attended_in_steps_of_sixteen_tokens():
+    n, heads, dim, page = 50, 2, 128, 16
+    c = Case([n, 0], heads, dim, page, 64, F16)
+    q = rnd((n, 8 * dim), 5, F16)
+    out, mass = torch.empty(n, 8 * dim, dtype=F16), torch.zeros(2, heads, c.width * page, device="cuda")
+    for first in range(0, n, Q.STAGQ_KV_MAX_NEW):
+        m = min(Q.STAGQ_KV_MAX_NEW, n - first)
+        part = torch.zeros(2 * m, 8 * dim, dtype=F16, device="cuda")
+        part[:m] = q[first:first + m].cuda()
+        got = torch.empty_like(part)
+        lens = torch.tensor([first + m, 0], dtype=torch.int32, device="cuda")
+        Q.stagq_kv_attention(c.cache, part, c.table, lens, got, n_new=m, mass=mass)
+        out[first:first + m] = got[:m].cpu()
+        assert not got[m:].any()
+    want, p, bound, p_bound = R.attention(q.view(1, n, 8, dim), c.k[:1], c.v[:1], [n], n, dim ** -0.5)
+    assert_rounded(out.view(want.shape), want, F16, bound[..., None])
+    # and a rounding of the sum per call
+    assert ((mass[0, :, :n].double().cpu() - p[0]).abs() <= p_bound[0] + 4 * 2.0 ** -24 * p[0]).all()
+    assert not mass[1].any()
+    Q.stagq_ops_check(0)
