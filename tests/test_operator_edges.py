@@ -294,3 +294,52 @@ def test_a_prompt_is_attended_in_steps_of_sixteen_tokens():
     assert ((mass[0, :, :n].double().cpu() - p[0]).abs() <= p_bound[0] + 4 * 2.0 ** -24 * p[0]).all()
     assert not mass[1].any()
     Q.stagq_ops_check(0)
+
+
+# -------------------------------------------------- shapes at the ends of the range
+
+@gpu
+@pytest.mark.parametrize("tracked", [False, True])
+def test_attention_of_the_most_rows_per_kv_head(tracked):
+    c = Case([300, 9], 1, 64, 16, 32, BF16)
+    c.check(64, 16, tracked=tracked)  # 1024 rows
+
+
+@gpu
+def test_a_batch_of_thousands_of_short_sequences():
+    b, heads, dim, page, budget = 3000, 2, 64, 16, 6
+    lens = [i * 7 % 21 for i in range(b)]
+    pool = torch.full((b * 3, Q.stagq_kv_page_bytes(heads, dim, page, 64)), 0xFF, dtype=torch.uint8, device="cuda")
+    cache = Q.KVCache(pool, heads, dim, page, 64, F16)
+    order = torch.randperm(b * 3, generator=torch.Generator().manual_seed(1)).to(torch.int32).cuda()
+    both = order.view(b, 3)
+    table, fresh = both[:, :2], both[:, 2:]  # slices: rows 3 apart
+    k, v = (rnd((b, 20, heads, dim), s, F16) for s in (1, 2))
+    Q.stagq_kv_append(cache, k.view(b * 20, -1).cuda(), v.view(b * 20, -1).cuda(), table, torch.zeros(b, dtype=torch.int32, device="cuda"), 20)
+    n = torch.tensor(lens, dtype=torch.int32, device="cuda")
+    q = rnd((b, 2 * heads * dim), 3, F16)
+    kk, vv = R.values4(k, 64), R.values4(v, 64)
+    want, p, bound, p_bound = R.attention(q.view(b, 1, 2 * heads, dim), kk, vv, lens, 1, dim ** -0.5)
+    mass = torch.zeros(2, b, heads, 40, device="cuda")[1, :, :, :32]  # rows further apart
+    for m in (None, mass):
+        out = torch.full((b, 2 * heads * dim), 3.0, dtype=F16, device="cuda")
+        Q.stagq_kv_attention(cache, q.cuda(), table, n, out, mass=m)
+        assert_rounded(out.view(want.shape), want, F16, bound[..., None])
+    got = mass.double().cpu()
+    assert ((got[..., :20] - p).abs() <= p_bound + 2.0 ** -24 * p).all() and not got[..., 20:].any()
+    kept, new_lens = torch.empty(b, heads, budget, dtype=torch.int32, device="cuda"), torch.empty(b, dtype=torch.int32, device="cuda")
+    new_mass = torch.full((b, heads, 12), 5.0, device="cuda")
+    Q.stagq_kv_evict(cache, table, n, mass, fresh, budget, 2, kept, new_lens, new_mass[..., :8])
+    assert new_lens.tolist() == [min(x, budget) for x in lens] and (new_mass[..., 8:] == 5).all()
+    ko, vo = (torch.empty(b * budget, heads * dim, device="cuda") for _ in range(2))
+    Q.stagq_kv_read(cache, fresh, new_lens, ko, vo, budget)
+    kept, host = kept.cpu(), mass.cpu().numpy()
+    for i in range(b):
+        for h in range(heads):
+            keep = R.keep(host[i, h], lens[i], budget, 2)
+            assert kept[i, h].tolist() == keep + [-1] * (budget - len(keep)), (i, h)
+    at = kept.clamp_min(0).long().permute(0, 2, 1)[..., None].expand(-1, -1, -1, dim)
+    there = (kept >= 0).permute(0, 2, 1)[..., None]
+    for got, values in ((ko, kk), (vo, vv)):
+        assert_rounded(got.view(b, budget, heads, dim), torch.where(there, torch.gather(values, 1, at), 0.0), F32)
+    Q.stagq_ops_check(0)
