@@ -494,9 +494,9 @@ int stagq_kv_read(const stagq_kv_cache* cache, const stagq_kv_table* table, cons
  * cache once for every 8 query rows of a KV head: this serves prompts of some
  * hundred tokens, and is no replacement for attention over 16-bit K and V.)
  * Precision: scores, weights and sums are fp32, from the terms s q u and lo q;
- * p s is summed in parts that drop 2^-30, per token, of the largest scale s of
- * the sequence's V in that group. Sums stay finite while |V| is
- * below 2^88 and |q| below 2^100.
+ * p s is summed in parts that drop, per token, 2^-30 of the largest scale s
+ * that the row sees in V's group, and no more than 2^-22 of its largest p s.
+ * Sums stay finite while |V| is below 2^88 and |q| below 2^100.
  * Errors: STAGQ_EINVAL, STAGQ_ECUDA.
  */
 int stagq_kv_attention(const stagq_kv_cache* cache, const stagq_kv_table* table, const int32_t* lens, int32_t max_len,

@@ -34,10 +34,10 @@
 //    product the repeats carry what rounding p s to fp16 lost, at no extra mma
 //    for up to 4 query rows per KV head (32 / 8 and 40 / 10 heads). Together
 //    the parts hold 22 bits of p s above 2^-9 of the largest scale s that the
-//    warp has met in the group, and below that all but 2^-30 of that scale per
-//    token. So the result has fp32's error as long as V's scales lie within
-//    some 2^12 of one another; a token with a larger one leaves the others
-//    fewer bits, also where its own weight is small.
+//    row has met in the group, and below that all but 2^-30 of that scale per
+//    token (and no more than 2^-22 of its largest p s, where that is less). The
+//    scaling is each row's own: a token that a row does not see, or hardly,
+//    may have any V.
 // The tcgen05 tensor cores would need the codes expanded to 8 or 16 bits in
 // shared memory first, 2 to 4 times the cache's bytes of shared-memory writes
 // and reads, for products that mma.sync does within the bytes' time.
@@ -423,9 +423,7 @@ __global__ void __launch_bounds__(kWarps * 32, resident_ctas(NT)) kv_attention_k
 
   float o[J][2][NT][4];
   float m[NT][2], l[NT][2], lsum[NT][2][NG];
-  int e_run[NG];                 // exponent field that p s is scaled by, 15 at least
-#pragma unroll
-  for (int n = 0; n < NG; ++n) e_run[n] = 15;
+  float fit[NT][2][NG];          // what p s is scaled by, 2^118 at most
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
@@ -433,7 +431,10 @@ __global__ void __launch_bounds__(kWarps * 32, resident_ctas(NT)) kv_attention_k
       m[nt][i] = -INFINITY;
       l[nt][i] = 0.0f;
 #pragma unroll
-      for (int n = 0; n < NG; ++n) lsum[nt][i][n] = 0.0f;
+      for (int n = 0; n < NG; ++n) {
+        lsum[nt][i][n] = 0.0f;
+        fit[nt][i][n] = pow2(118);
+      }
     }
 #pragma unroll
     for (int j = 0; j < J; ++j)
@@ -610,41 +611,53 @@ __global__ void __launch_bounds__(kWarps * 32, resident_ctas(NT)) kv_attention_k
     }
 #pragma unroll
     for (int c = 0; c < NG; ++c) {
-      // p s is held as p s 2^(6 - e), where s < 2^(e + 1) as far as seen: below
-      // 2^15, for p is below 2^8. When an s is larger, e follows.
-      float sv[4], lo[4];
-      float f = __uint_as_float(static_cast<uint32_t>(260 - e_run[c]) << 23);
+      // A row's p s is held as p s 2^(6 - e), where s < 2^(e + 1) for the scales
+      // that it has met: below 2^15, for p is below 2^8. When an s is larger, e
+      // follows, of the rows that see the token, and no further than 2^8 past the
+      // row's largest p s: a token of small weight costs the others no bits.
+      float sv[4], lo[4], fit_top = 0.0f;
 #pragma unroll
       for (int n = 0; n < 4; ++n) {
         sv[n] = pair_scale<BF>(mv[n][c]);
         lo[n] = fmaf(sv[n], 8.0f, pair_low<BF>(mv[n][c]));
       }
-      const float large = fmaxf(fmaxf(sv[0], sv[1]), fmaxf(sv[2], sv[3])) * f;
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) fit_top = fmaxf(fit_top, fmaxf(fit[nt][0][c], fit[nt][1][c]));
+      const float large = fmaxf(fmaxf(sv[0], sv[1]), fmaxf(sv[2], sv[3])) * fit_top;
       if (__any_sync(kFull, large >= 128.0f)) {
-        uint32_t top_s = 0;
 #pragma unroll
-        for (int n = 0; n < 4; ++n) {
-          const uint32_t bits = __float_as_uint(fabsf(sv[n]));
-          top_s = max(top_s, bits < 0x7F800000u ? bits : 0u);
-        }
-        const int e_new = static_cast<int>(__reduce_max_sync(kFull, top_s) >> 23);
-        if (e_new > e_run[c]) {
-          const float down = e_new - e_run[c] > 126 ? 0.0f : pow2(e_run[c] - e_new);
+        for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-          for (int j = c * JG; j < (c + 1) * JG; ++j)
+          for (int i = 0; i < 2; ++i) {
+            constexpr uint32_t kInf = 0x7F800000u;
+            uint32_t top_s = 0, top_ps = 0;  // bits of the row's largest s and p s
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
+            for (int n = 0; n < 4; ++n) {
+              const uint32_t of_s = __float_as_uint(fabsf(sv[n])), of_ps = __float_as_uint(fabsf(s[nt][i][n] * sv[n]));
+              if (of_s >= kInf || (edge && tok0 + 8 * n >= lim[nt][i])) continue;
+              top_s = max(top_s, of_s);
+              top_ps = max(top_ps, of_ps < kInf ? of_ps : of_s);
+            }
 #pragma unroll
-              for (int i = 0; i < 4; ++i) {
+            for (int d = 4; d < 32; d <<= 1) {
+              top_s = max(top_s, __shfl_xor_sync(kFull, top_s, d));
+              top_ps = max(top_ps, __shfl_xor_sync(kFull, top_ps, d));
+            }
+            const int e = 260 - static_cast<int>(__float_as_uint(fit[nt][i][c]) >> 23);
+            const int e_new = min(static_cast<int>(top_s >> 23), static_cast<int>(top_ps >> 23) + 8);
+            if (e_new > e) {  // the same in all lanes of the row
+              const float down = e_new - e > 126 ? 0.0f : pow2(e - e_new);
+#pragma unroll
+              for (int j = c * JG; j < (c + 1) * JG; ++j) {
                 o[j][0][nt][i] *= down;
+                o[j][0][nt][2 + i] *= down;
                 o[j][1][nt][i] *= down;
+                o[j][1][nt][2 + i] *= down;
               }
-          e_run[c] = e_new;
-          f = __uint_as_float(static_cast<uint32_t>(260 - e_new) << 23);
-        }
+              fit[nt][i][c] = __uint_as_float(static_cast<uint32_t>(260 - e_new) << 23);
+            }
+          }
       }
-#pragma unroll
-      for (int n = 0; n < 4; ++n) sv[n] *= f;
       uint32_t pf[NT][4];  // B fragments of both products, k = token
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
@@ -654,7 +667,7 @@ __global__ void __launch_bounds__(kWarps * 32, resident_ctas(NT)) kv_attention_k
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
             const bool hidden = edge && tok0 + 8 * n >= lim[nt][i];  // 0 times a NaN that other rows see
-            x[i] = hidden ? 0.0f : s[nt][i][n] * sv[n];
+            x[i] = hidden ? 0.0f : s[nt][i][n] * fit[nt][i][c] * sv[n];  // (p fit is finite whatever s is)
             lsum[nt][i][c] += hidden ? 0.0f : s[nt][i][n] * lo[n];
             // columns 4..7 take what fp16's 11 bits, cut toward zero, leave
             x[i] -= __uint_as_float(__float_as_uint(x[i]) & rest_mask);
@@ -698,7 +711,8 @@ __global__ void __launch_bounds__(kWarps * 32, resident_ctas(NT)) kv_attention_k
       }
 #pragma unroll
       for (int j = 0; j < J; ++j) {
-        const float up = pow2(e_run[j / JG] - 127 - 6), up16 = up * 0.0625f, low = t < 2 ? 0.0f : lsum[nt][i][j / JG];
+        const float up = __uint_as_float((254u << 23) - __float_as_uint(fit[nt][i][j / JG]));  // 1 / fit
+        const float up16 = up * 0.0625f, low = t < 2 ? 0.0f : lsum[nt][i][j / JG];
         *reinterpret_cast<float4*>(&s_o[warp][8 * nt + 2 * t + i][32 * j + 4 * g]) =
             make_float4(fmaf(o[j][0][nt][i], up, low), fmaf(o[j][0][nt][2 + i], up16, low), fmaf(o[j][1][nt][i], up, low),
                         fmaf(o[j][1][nt][2 + i], up16, low));

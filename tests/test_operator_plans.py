@@ -291,3 +291,52 @@ def test_launches_that_the_benchmark_counts(lens, tracked):
         status, _, nodes = runtime.cudaGraphGetNodes(graph.raw_cuda_graph(), 0)
         assert status == runtime.cudaError_t.cudaSuccess
         assert nodes == kernels
+
+
+# --------------------------------------------- scales that a row does not see, or hardly
+
+@gpu
+@pytest.mark.parametrize("tracked", [False, True])
+@pytest.mark.parametrize("q_heads,tokens", [(4, 40), (4, 333), (16, 333)])
+@pytest.mark.parametrize("dim,group,dtype", [(128, 128, F16), (128, 32, BF16), (64, 64, BF16)])
+def test_an_extreme_v_that_a_row_does_not_see_costs_it_nothing(dim, group, dtype, q_heads, tokens, tracked):
+    # the newest of three tokens holds the type's largest values: the two before it do not see them
+    v = rnd((1, tokens, 2, dim), 4, dtype)
+    v[0, -1, :, ::2], v[0, -1, :, 1::2] = torch.finfo(dtype).max / 4, torch.finfo(dtype).min / 4
+    c = Filled([tokens], 2, dim, 16, group, dtype, v=v)
+    q = rnd((3, q_heads * dim), 5, dtype)
+    got = c.attend(q.cuda(), 3, torch.zeros(1, 2, c.width * 16, device="cuda") if tracked else None)
+    want, _, bound, _ = R.attention(q.view(1, 3, q_heads, dim), c.k, c.v, [tokens], 3, dim ** -0.5)
+    assert_rounded(got.view(want.shape), want, dtype, bound[..., None], "out")
+    Q.stagq_ops_check(0)
+
+
+@gpu
+@pytest.mark.parametrize("at", [0, 700, 1499])
+@pytest.mark.parametrize("n_new,tracked", [(1, False), (2, True)])
+@pytest.mark.parametrize("dtype,large", [(F16, 13.0), (BF16, 13.0), (BF16, 34.0)])
+def test_a_large_v_of_small_weight_leaves_the_others_their_bits(dtype, large, n_new, tracked, at):
+    """One token's V is 2^13 or 2^34 times the others', and its weight 2^-40 for every second query row while the others attend
+    to it alone. Bound: twice the scores' error on sum p |V|, and what the parts of p s cut: 2^-30, per token and unit of
+    the code's distance from 8, of a scale that follows max p s within 2^8."""
+    tokens, heads, dim, group = 1500, 2, 128, 64
+    k, v = rnd((1, tokens, heads, dim), 1) * 0.3, 1 + 0.3 * rnd((1, tokens, heads, dim), 2)
+    k[..., 0], k[0, at, :, 0] = 0.0, 20.0
+    v[0, at] *= 2.0 ** large
+    q = rnd((n_new, heads * 4, dim), 3)
+    q[:, 0::2, 0], q[:, 1::2, 0] = 16.0, -16.0  # scores of the large token: +28 and -28 nats
+    q = q.to(dtype)
+    c = Filled([tokens + 2], heads, dim, 16, group, dtype, k=torch.cat([k, rnd((1, 2, heads, dim), 8) * 0.3], 1).to(dtype),
+               v=torch.cat([v, 1 + 0.3 * rnd((1, 2, heads, dim), 9)], 1).to(dtype))
+    n = tokens + 2
+    got = c.attend(q.view(n_new, -1).cuda(), n_new, torch.zeros(1, heads, c.width * 16, device="cuda") if tracked else None)
+    scale = dim ** -0.5
+    want, _, bound, _ = R.attention(q[None], c.k, c.v, [n], n_new, scale)
+    weighted, _, _, _ = R.attention(q[None], c.k, c.v.abs(), [n], n_new, scale)
+    err = bound / (2 * c.v.abs().max())
+    s = R.rounded4(c.v_in, group)[1].amax(-1)[0].cpu()  # [tokens, heads]
+    scores = torch.einsum("jhpd,thd->jhpt", q.double().view(n_new, heads, 4, dim), c.k[0]) * scale
+    ps = (torch.softmax(scores, -1) * s.T[None, :, None]).amax(-1).view(1, n_new, heads * 4, 1)
+    extra = 2 * err[..., None] * weighted + n * 2.0 ** -19 * ps
+    assert_rounded(got.view(want.shape), want, dtype, extra, "out")
+    Q.stagq_ops_check(0)
