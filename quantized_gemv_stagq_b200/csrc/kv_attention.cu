@@ -126,6 +126,14 @@ __device__ __forceinline__ float pair_low(uint32_t w) {
 // 2^e for -126 <= e <= 127.
 __device__ __forceinline__ float pow2(int e) { return __uint_as_float(static_cast<uint32_t>(e + 127) << 23); }
 
+// Both products by one instruction.
+__device__ __forceinline__ void mul2(float& x, float& y, float a, float b) {
+  asm("{\n\t.reg .b64 p, q;\n\tmov.b64 p, {%0, %1};\n\tmov.b64 q, {%2, %3};\n\t"
+      "mul.rn.f32x2 p, p, q;\n\tmov.b64 {%0, %1}, p;\n\t}"
+      : "+f"(x), "+f"(y)
+      : "f"(a), "f"(b));
+}
+
 template <int WORDS>
 __device__ __forceinline__ void load_words(uint32_t (&w)[WORDS], const uint8_t* p) {
   static_assert(WORDS == 1 || WORDS == 2 || WORDS == 4, "one vector load");
@@ -663,11 +671,13 @@ __global__ void __launch_bounds__(kWarps * 32, resident_ctas(NT)) kv_attention_k
       for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
         for (int n = 0; n < 4; ++n) {
-          float x[2];
+          float x[2] = {s[nt][0][n], s[nt][1][n]};
+          mul2(x[0], x[1], fit[nt][0][c], fit[nt][1][c]);  // finite whatever s is
+          mul2(x[0], x[1], sv[n], sv[n]);
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
             const bool hidden = edge && tok0 + 8 * n >= lim[nt][i];  // 0 times a NaN that other rows see
-            x[i] = hidden ? 0.0f : s[nt][i][n] * fit[nt][i][c] * sv[n];  // (p fit is finite whatever s is)
+            if (hidden) x[i] = 0.0f;
             lsum[nt][i][c] += hidden ? 0.0f : s[nt][i][n] * lo[n];
             // columns 4..7 take what fp16's 11 bits, cut toward zero, leave
             x[i] -= __uint_as_float(__float_as_uint(x[i]) & rest_mask);
