@@ -9,7 +9,7 @@
 //
 // The cache's bytes would bound it if the unpacking kept up: at 6.5 TB/s an SM
 // takes in about 49 codes per clock. Measured, long sequences stream 3.4 TB/s:
-// issue slots 59 % and the ALU pipe 55 % busy, no unit full, 12 warps per SM
+// issue slots 58 % and the ALU pipe 55 % busy, no unit full, 12 warps per SM
 // that each wait on their own chain of steps. What keeps the instruction count
 // near one per two codes:
 //  - V: two codes are masked out of a word in place and OR'ed under the exponent
