@@ -400,8 +400,8 @@ int stagq_quantize_i8(const void* x, int64_t x_stride, int32_t n, int32_t in, ui
                       float* scale, int device, void* cuda_stream);
 
 /*
- * y_ij = xscale_i wscale_j sum_k xq_ik wq_jk for i < n, j < out: the sum is
- * exact (int32), scaled in fp32 and rounded once.
+ * y_ij = xscale_i (wscale_j sum_k xq_ik wq_jk) for i < n, j < out: the sum is
+ * exact (int32), scaled in fp32 in this order and rounded once.
  *   xq, wq  device rows of stagq_i8_row_bytes(in) bytes, 16-byte aligned, whose
  *           bytes from `in` on are 0 (as stagq_quantize_i8 leaves them)
  *   y       device [n] rows of `out` values, y_stride elements apart: fp16,
@@ -496,7 +496,7 @@ int stagq_kv_read(const stagq_kv_cache* cache, const stagq_kv_table* table, cons
  * Precision: scores, weights and sums are fp32, from the terms s q u and lo q;
  * p s is summed in parts that drop, per token, 2^-30 of the largest scale s
  * that the row sees in V's group, and no more than 2^-22 of its largest p s.
- * Sums stay finite while |V| is below 2^88 and |q| below 2^100.
+ * Sums stay finite while |V| is below 2^88 and |q| |K| below 2^100.
  * Errors: STAGQ_EINVAL, STAGQ_ECUDA.
  */
 int stagq_kv_attention(const stagq_kv_cache* cache, const stagq_kv_table* table, const int32_t* lens, int32_t max_len,

@@ -235,6 +235,8 @@ __device__ __forceinline__ int load_peer(uint32_t addr, uint32_t rank) {
   return v;
 }
 
+// A sum is scaled by its channel first, whose weights are of one size; tokens
+// (bf16) may be far from 1, and their scale times the sum out of fp32's range.
 __device__ __forceinline__ void store_y(const GemmI8Args& a, int64_t at, float y) {
   if (a.y_f32)
     static_cast<float*>(a.y)[at] = y;
@@ -362,7 +364,7 @@ __global__ void __launch_bounds__(kGemmThreads) gemm_i8_kernel(const __grid_cons
           for (int i = 0; i < 16; ++i) xs[i] = c0 + i < cols ? a.xs[n0 + c0 + i] : 0.0f;
 #pragma unroll
           for (int i = 0; i < 16; ++i)
-            if (c0 + i < cols) store_y(a, static_cast<int64_t>(n0 + c0 + i) * a.y_stride + o, static_cast<float>(v[i]) * xs[i] * ws);
+            if (c0 + i < cols) store_y(a, static_cast<int64_t>(n0 + c0 + i) * a.y_stride + o, static_cast<float>(v[i]) * ws * xs[i]);
         }
       }
     }
@@ -392,7 +394,7 @@ __global__ void __launch_bounds__(kGemmThreads) gemm_i8_kernel(const __grid_cons
             int sum = 0;
 #pragma unroll
             for (int r = 0; r < 8; ++r) sum += v[i][r];
-            store_y(a, static_cast<int64_t>(n0 + c) * a.y_stride + o, static_cast<float>(sum) * xs[i] * ws);
+            store_y(a, static_cast<int64_t>(n0 + c) * a.y_stride + o, static_cast<float>(sum) * ws * xs[i]);
           }
         }
       }
@@ -469,10 +471,10 @@ __device__ __forceinline__ void store_rows(const GemmI8Args& a, int64_t at, cons
 #pragma unroll
   for (int i = 0; i < 16; i += 4) {
     const float4 w = *reinterpret_cast<const float4*>(ws + i);
-    y[i] = static_cast<float>(v[i]) * xs * w.x;
-    y[i + 1] = static_cast<float>(v[i + 1]) * xs * w.y;
-    y[i + 2] = static_cast<float>(v[i + 2]) * xs * w.z;
-    y[i + 3] = static_cast<float>(v[i + 3]) * xs * w.w;
+    y[i] = static_cast<float>(v[i]) * w.x * xs;
+    y[i + 1] = static_cast<float>(v[i + 1]) * w.y * xs;
+    y[i + 2] = static_cast<float>(v[i + 2]) * w.z * xs;
+    y[i + 3] = static_cast<float>(v[i + 3]) * w.w * xs;
   }
   if (a.wide && left >= 16) {
     if (lane >= rows) return;

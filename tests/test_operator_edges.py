@@ -343,3 +343,28 @@ def test_a_batch_of_thousands_of_short_sequences():
     for got, values in ((ko, kk), (vo, vv)):
         assert_rounded(got.view(b, budget, heads, dim), torch.where(there, torch.gather(values, 1, at), 0.0), F32)
     Q.stagq_ops_check(0)
+
+
+# ------------------------------------------------------------------- magnitudes
+
+@gpu
+@pytest.mark.parametrize("n,inp,out", [(3, 512, 200), (40, 4096, 300), (300, 512, 5000)])
+def test_gemm_i8_of_activations_near_the_ends_of_bf16(n, inp, out):
+    # sum * xscale alone would leave fp32 where the result does not: rows of 2^118 and of 2^-118, weights of 2^-12
+    x = rnd((n, inp), n)
+    x[0] *= 2.0 ** 118
+    x[1] *= 2.0 ** -118
+    x = x.to(BF16).cuda()
+    w = (rnd((out, inp), 7) * 2.0 ** -12).to(BF16).cuda()
+    row = Q.stagq_i8_row_bytes(inp)
+    (xq, wq), (xs, ws) = (torch.empty(r, row, dtype=torch.int8, device="cuda") for r in (n, out)), (torch.empty(r, device="cuda") for r in (n, out))
+    Q.stagq_quantize_i8(x, xq, xs)
+    Q.stagq_quantize_i8(w, wq, ws)
+    sums = xq[:, :inp].double() @ wq[:, :inp].double().T
+    want = (sums * xs.double()[:, None] * ws.double()).cpu()
+    assert want.abs().max() < 2.0 ** 127
+    for dtype in (F32, BF16):
+        y = torch.empty(n, out, dtype=dtype, device="cuda")
+        Q.stagq_gemm_i8(xq, xs, wq, ws, inp, y)
+        # the sum to fp32 and two products, the last of which is fp32's own rounding
+        assert_rounded(y, want, dtype, want.abs() * (3.01 if dtype != F32 else 2.01) * 2.0 ** -24, str(dtype))
